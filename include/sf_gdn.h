@@ -235,6 +235,123 @@ sf_status sf_gdn_shortconv_bwd(const sf_conv_shape* shape, const void* x, const 
                                void* dx, float* dw, void* dconv_in, void* workspace,
                                size_t ws_bytes, void* stream);
 
+/* Single tokens over a pool of sequence states (serving).
+ *
+ * A batch holds n_seq sequences and n_tok token rows.  Sequence i brings the
+ * rows seq_start[i] .. seq_start[i+1]-1 (seq_start: n_seq + 1 offsets,
+ * non-decreasing; NULL: n_tok / n_seq rows each), of any number, and its state
+ * lives in slot slots[i] of the pool (NULL: slot i), which the call advances
+ * in place over the sequence's tokens (update = 1) or only reads (update = 0,
+ * e.g. to score drafted tokens that may be taken back).  Both arrays are in
+ * device memory and need 4-byte alignment only; the host does not read them:
+ *   - slots[i] < 0 marks padding: nothing of the entry is read or written;
+ *   - an entry with no rows leaves its state as it was;
+ *   - rows of no sequence (past the last offset) keep their output's contents;
+ *   - an entry whose slot is not below n_slots, or with update = 1 repeats the
+ *     slot of an earlier entry, is refused: its output rows are NaN and no
+ *     state is touched for it.  With update = 0 entries may share a slot;
+ *   - offsets are clamped to 0 .. n_tok; no entry reaches outside the tensors.
+ * Token rows of q, k, v (x) may lie stride elements apart, e.g. as slices of
+ * one projection's rows: 0 means contiguous, else a multiple of 8, at least
+ * one row.  All else is contiguous.  Calls on one pool are ordered by the
+ * caller (one stream, or events). */
+typedef struct {
+  int n_seq, n_tok, n_slots;
+  int Hk, Hv;   /* key heads, value heads; Hv a multiple of Hk: value head h
+                 * reads q and k of head h / (Hv / Hk) */
+  int Dk, Dv;   /* Dk == Dv in {64, 128} */
+  int dtype;    /* sf_dtype of q, k, v, o */
+  int update;   /* 1: the pool is advanced; 0: it is only read */
+  long long q_stride, k_stride, v_stride;
+} sf_step_shape;
+
+/* The gated delta rule token by token:
+ *     S <- alpha S (I - beta k k^T) + beta v k^T,   o = S q
+ * per value head, from the state in the pool.  The same recurrence as
+ * sf_gdn_chunk_fwd, in fp32 throughout (o is rounded once); a chunk's S_out
+ * of one sequence is a pool slot.  Meant for the few tokens per sequence of a
+ * decoding step: every token costs a pass over the state in registers, so
+ * long prompts belong to the chunk calls.
+ *   q, k [n_tok, Hk, Dk], v [n_tok, Hv, Dv], o [n_tok, Hv, Dv]  dtype
+ *   alpha, beta [n_tok, Hv] fp32 (4-byte aligned)
+ *   state [n_slots, Hv, Dv, Dk] fp32, in place. */
+sf_status sf_gdn_recurrent_step(const sf_step_shape* shape, const void* q, const void* k,
+                                const void* v, const float* alpha, const float* beta,
+                                const int* slots, const int* seq_start, float* state, void* o,
+                                void* stream);
+
+/* The short convolution of sf_gdn_shortconv_fwd over the same kind of batch:
+ *   x, y [n_tok, C] and state [n_slots, W-1, C] in dtype (the last W-1 inputs
+ *   of each sequence, oldest first, as conv_in / conv_out), w [C, W] fp32.
+ * state may be NULL for W = 1. */
+typedef struct {
+  int n_seq, n_tok, n_slots;
+  int C, W;
+  int dtype;
+  int act;     /* 0: none, 1: SiLU */
+  int update;
+  long long x_stride;
+} sf_conv_step_shape;
+sf_status sf_gdn_shortconv_step(const sf_conv_step_shape* shape, const void* x, const float* w,
+                                const int* slots, const int* seq_start, void* state, void* y,
+                                void* stream);
+
+/* Norm of every head's D values, with a weight, a gate and a scale:
+ *     n = x / sqrt(mean(x^2) + eps),   y = scale * w * n * act(gate)
+ * act(g) = g * sigmoid(g) (act = 1) or g (act = 0); NULL gate: factor 1; NULL
+ * w: ones.  After the recurrence with the layer's output gate; with neither
+ * gate nor weight and scale = 1 / sqrt(D) it is the L2 norm of q and k before
+ * it (eps there enters as eps * D).
+ *   x, gate [N, H, D], dtype, token rows x_stride (gate_stride) elements
+ *   apart (0: contiguous; a multiple of 8); y, dy, dx, dgate contiguous;
+ *   w, dw [D] fp32, shared by the heads.  D a multiple of 8, at most 512.
+ * The backward recomputes the statistics from x.  It writes dx, dgate
+ * (required with gate) and, unless dw is NULL, dw: the gradient summed over
+ * tokens and heads in a fixed order, not accumulated into dw's old contents.
+ * Only dw needs the workspace (256-byte aligned). */
+typedef struct {
+  long long N;
+  int H, D;
+  int dtype;
+  int act;
+  float eps, scale;
+  long long x_stride, gate_stride;
+} sf_gated_norm_shape;
+sf_status sf_gdn_gated_norm_fwd(const sf_gated_norm_shape* shape, const void* x, const void* gate,
+                                const float* w, void* y, void* stream);
+sf_status sf_gdn_gated_norm_bwd_workspace_size(const sf_gated_norm_shape* shape, size_t* bytes);
+sf_status sf_gdn_gated_norm_bwd(const sf_gated_norm_shape* shape, const void* x, const void* gate,
+                                const float* w, const void* dy, void* dx, void* dgate, float* dw,
+                                void* workspace, size_t ws_bytes, void* stream);
+
+/* Residual sum with its scale, and the norm before the next block:
+ *     h = x + scale * s * r,   y = w * h / sqrt(mean(h^2) + eps)
+ * over rows of C values.  s [C] fp32 is a residual scale per channel (NULL:
+ * ones), w [C] fp32 (NULL: ones).  r and h may both be NULL: the norm of x
+ * alone.  y is formed from h before its rounding to dtype.
+ *   x, r, h, y, dy, dh, dx, dr [N, C] dtype, contiguous; C a multiple of 8,
+ *   at most 16384.
+ * The backward takes h as the forward wrote it, dy and dh (the gradient that
+ * reaches h from the residual stream; NULL: zeros) and writes
+ *     dx = the gradient of h,   dr = scale * s * dx  (NULL: not wanted),
+ * dw and ds (NULL: not wanted; ds needs r), summed over rows in a fixed
+ * order, not accumulated.  dw and ds need the workspace (256-byte aligned). */
+typedef struct {
+  long long N;
+  int C;
+  int dtype;
+  float eps, scale;
+} sf_residual_norm_shape;
+sf_status sf_gdn_residual_norm_fwd(const sf_residual_norm_shape* shape, const void* x,
+                                   const void* r, const float* s, const float* w, void* h, void* y,
+                                   void* stream);
+sf_status sf_gdn_residual_norm_bwd_workspace_size(const sf_residual_norm_shape* shape,
+                                                  size_t* bytes);
+sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const void* h,
+                                   const void* r, const float* s, const float* w, const void* dy,
+                                   const void* dh, void* dx, void* dr, float* dw, float* ds,
+                                   void* workspace, size_t ws_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* sf_status_string(int status);
 /* Detail of the calling thread's last non-OK status (static until the next

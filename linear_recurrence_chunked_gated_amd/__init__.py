@@ -10,22 +10,31 @@ in include/sf_gdn.h.
     short_conv(x, w, conv_in)                        -> (y, conv_out), torch autograd
     shortconv_fwd(x, w, conv_in)                     -> (y, conv_out)
     shortconv_bwd(x, w, conv_in, dy, dconv_out)      -> (dx, dw, dconv_in)
+    recurrent_step(q, k, v, alpha, beta, state, slots, seq_start)  -> o, decoding
+    shortconv_step(x, w, state, slots, seq_start)                  -> y, decoding
+    gated_norm_fwd(x, gate, w) / gated_norm_bwd(x, gate, w, dy)
+    residual_norm_fwd(x, r, w, s) / residual_norm_bwd(h, r, w, s, dy, dh)
+    gated_norm(x, gate, w), residual_norm(x, r, w, s): the norms, torch autograd
 
 Imports are lazy so that the input generator and the planner load without the
 HIP library.
 """
 __all__ = ["chunk_fwd", "chunk_bwd", "chain_fwd", "chain_bwd", "gated_delta_chunk", "short_conv",
-           "shortconv_fwd", "shortconv_bwd", "profile", "GDNError"]
+           "shortconv_fwd", "shortconv_bwd", "recurrent_step", "shortconv_step", "gated_norm",
+           "gated_norm_fwd", "gated_norm_bwd", "residual_norm", "residual_norm_fwd",
+           "residual_norm_bwd", "profile", "GDNError"]
 
 
 def __getattr__(name):
-    if name in ("chunk_fwd", "chunk_bwd", "shortconv_fwd", "shortconv_bwd", "profile", "GDNError"):
+    if name in ("chunk_fwd", "chunk_bwd", "shortconv_fwd", "shortconv_bwd", "recurrent_step",
+                "shortconv_step", "gated_norm_fwd", "gated_norm_bwd", "residual_norm_fwd",
+                "residual_norm_bwd", "profile", "GDNError"):
         from . import _lib
         return getattr(_lib, name)
     if name in ("chain_fwd", "chain_bwd"):
         from . import chain
         return getattr(chain, name)
-    if name in ("gated_delta_chunk", "short_conv"):
+    if name in ("gated_delta_chunk", "short_conv", "gated_norm", "residual_norm"):
         from . import autograd
         return getattr(autograd, name)
     raise AttributeError(name)

@@ -33,6 +33,32 @@ class ConvShape(ctypes.Structure):
                 ("W", ctypes.c_int), ("dtype", ctypes.c_int), ("act", ctypes.c_int)]
 
 
+class StepShape(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int), ("n_tok", ctypes.c_int), ("n_slots", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("Hv", ctypes.c_int), ("Dk", ctypes.c_int),
+                ("Dv", ctypes.c_int), ("dtype", ctypes.c_int), ("update", ctypes.c_int),
+                ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+                ("v_stride", ctypes.c_longlong)]
+
+
+class ConvStepShape(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int), ("n_tok", ctypes.c_int), ("n_slots", ctypes.c_int),
+                ("C", ctypes.c_int), ("W", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("act", ctypes.c_int), ("update", ctypes.c_int), ("x_stride", ctypes.c_longlong)]
+
+
+class GatedNormShape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_longlong), ("H", ctypes.c_int), ("D", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("act", ctypes.c_int), ("eps", ctypes.c_float),
+                ("scale", ctypes.c_float), ("x_stride", ctypes.c_longlong),
+                ("gate_stride", ctypes.c_longlong)]
+
+
+class ResidualNormShape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_longlong), ("C", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
 SIGNATURES = {
     "sf_gdn_chunk_fwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.POINTER(_sz)]),
     "sf_gdn_chunk_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.POINTER(_sz)]),
@@ -53,6 +79,18 @@ SIGNATURES = {
     "sf_gdn_shortconv_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(ConvShape),
                                                            ctypes.POINTER(_sz)]),
     "sf_gdn_shortconv_bwd": (ctypes.c_int, [ctypes.POINTER(ConvShape)] + [_vp] * 9 + [_sz, _vp]),
+    "sf_gdn_recurrent_step": (ctypes.c_int, [ctypes.POINTER(StepShape)] + [_vp] * 10),
+    "sf_gdn_shortconv_step": (ctypes.c_int, [ctypes.POINTER(ConvStepShape)] + [_vp] * 7),
+    "sf_gdn_gated_norm_fwd": (ctypes.c_int, [ctypes.POINTER(GatedNormShape)] + [_vp] * 5),
+    "sf_gdn_gated_norm_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(GatedNormShape),
+                                                            ctypes.POINTER(_sz)]),
+    "sf_gdn_gated_norm_bwd": (ctypes.c_int, [ctypes.POINTER(GatedNormShape)] + [_vp] * 8
+                              + [_sz, _vp]),
+    "sf_gdn_residual_norm_fwd": (ctypes.c_int, [ctypes.POINTER(ResidualNormShape)] + [_vp] * 7),
+    "sf_gdn_residual_norm_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(ResidualNormShape),
+                                                               ctypes.POINTER(_sz)]),
+    "sf_gdn_residual_norm_bwd": (ctypes.c_int, [ctypes.POINTER(ResidualNormShape)] + [_vp] * 11
+                                 + [_sz, _vp]),
     "sf_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "sf_last_error_message": (ctypes.c_char_p, []),
     "sf_gdn_version": (ctypes.c_char_p, []),
@@ -407,6 +445,308 @@ def shortconv_bwd(x, w, conv_in, dy, dconv_out=None, act=0, dx=None, dw=None, wa
                                        ctypes.c_size_t(0 if workspace is None else workspace.numel()),
                                        _stream(stream)), "sf_gdn_shortconv_bwd")
     return dx, dw, dci
+
+
+def _device_of(t, name):
+    if t.device.type != "cuda":
+        raise ValueError("tensors must be on a GPU device (%s is on %s)" % (name, t.device))
+    return t.device
+
+
+def _run(name, dev, stream, *args):
+    """The call `name` on `stream` (the current stream of `dev` when None),
+    with `dev` current, so that tensors of another device than the current one
+    run on their own."""
+    if stream is not None and stream.device != dev:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _stream(stream))
+    _check(st, name)
+
+
+def _token_rows(t, name, dtype, shape, device):
+    """Elements between the token rows of t [n, ...], whose rows are
+    contiguous but may lie apart (a slice of wider rows); 0 when there is at
+    most one."""
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.dtype != dtype:
+        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.is_contiguous() or t.shape[0] == 0:
+        return 0
+    if not t[0].is_contiguous():
+        raise ValueError("%s: each token's row must be contiguous" % name)
+    if t.shape[0] == 1:
+        return 0
+    if t.stride(0) < t[0].numel():
+        raise ValueError("%s: token rows must not overlap" % name)
+    return t.stride(0)
+
+
+def _dtype_code(t, name):
+    if t.dtype not in _DTYPES:
+        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
+    return _DTYPES[t.dtype]
+
+
+def _batch(slots, seq_start, n_slots, dev):
+    """n_seq of a batch over a pool."""
+    n_seq = None
+    for t, n, extra in ((slots, "slots", 0), (seq_start, "seq_start", 1)):
+        if t is None:
+            continue
+        if t.dim() != 1 or t.shape[0] < extra:
+            raise ValueError("%s must have one dimension, of n_seq%s" % (n, " + 1" if extra else ""))
+        _need(t, n, torch.int32, (t.shape[0] if n_seq is None else n_seq + extra,), dev)
+        n_seq = t.shape[0] - extra
+    return n_slots if n_seq is None else n_seq
+
+
+def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=None, update=True,
+                   stream=None):
+    """sf_gdn_recurrent_step on torch tensors: the gated delta rule token by
+    token over a pool of sequence states, for decoding.
+
+    q, k [n_tok, Hk, Dk], v [n_tok, Hv, Dv] (bf16 or fp32; token rows may be
+    slices of wider rows), alpha, beta [n_tok, Hv] fp32, state [n_slots, Hv,
+    Dv, Dk] fp32, advanced in place unless update is False.  slots [n_seq]
+    int32 names each sequence's slot (None: sequence i has slot i, one for
+    every slot; negative: padding), seq_start [n_seq + 1] int32 its token rows
+    (None: n_tok / n_seq each).  Returns o [n_tok, Hv, Dv]; rows of padding
+    and past the last sequence keep what o held (pass o to set it)."""
+    dev = _device_of(q, "q")
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        raise ValueError("q and v must be [n_tok, heads, D], state [n_slots, Hv, Dv, Dk]")
+    N, Hk, Dk = q.shape
+    Hv, Dv = v.shape[1:]
+    code = _dtype_code(q, "q")
+    qs = _token_rows(q, "q", q.dtype, (N, Hk, Dk), dev)
+    ks = _token_rows(k, "k", q.dtype, (N, Hk, Dk), dev)
+    vs = _token_rows(v, "v", q.dtype, (N, Hv, Dv), dev)
+    _need(alpha, "alpha", torch.float32, (N, Hv), dev)
+    _need(beta, "beta", torch.float32, (N, Hv), dev)
+    _need(state, "state", torch.float32, (state.shape[0], Hv, Dv, Dk), dev)
+    n_seq = _batch(slots, seq_start, state.shape[0], dev)
+    if o is None:
+        o = torch.empty((N, Hv, Dv), dtype=q.dtype, device=dev)
+        used_on(stream, o)
+    _need(o, "o", q.dtype, (N, Hv, Dv), dev)
+    shape = StepShape(n_seq, N, state.shape[0], Hk, Hv, Dk, Dv, code, int(bool(update)), qs, ks,
+                      vs)
+    _run("sf_gdn_recurrent_step", dev, stream, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
+         _ptr(alpha), _ptr(beta), _ptr(slots), _ptr(seq_start), _ptr(state), _ptr(o))
+    return o
+
+
+def shortconv_step(x, w, state, slots=None, seq_start=None, act=0, y=None, update=True,
+                   stream=None):
+    """sf_gdn_shortconv_step on torch tensors: the short convolution token by
+    token over a pool of boundary states, for decoding.
+
+    x [n_tok, C] (token rows may be slices of wider rows), w [C, W] fp32,
+    state [n_slots, W-1, C] in x's dtype, advanced in place unless update is
+    False; slots and seq_start as in recurrent_step.  Returns y [n_tok, C]."""
+    dev = _device_of(x, "x")
+    if x.dim() != 2 or w.dim() != 2 or state.dim() != 3:
+        raise ValueError("x must be [n_tok, C], w [C, W], state [n_slots, W-1, C]")
+    N, C = x.shape
+    W = w.shape[1]
+    code = _dtype_code(x, "x")
+    xs = _token_rows(x, "x", x.dtype, (N, C), dev)
+    _need(w, "w", torch.float32, (C, W), dev)
+    _need(state, "state", x.dtype, (state.shape[0], W - 1, C), dev)
+    n_seq = _batch(slots, seq_start, state.shape[0], dev)
+    if y is None:
+        y = torch.empty((N, C), dtype=x.dtype, device=dev)
+        used_on(stream, y)
+    _need(y, "y", x.dtype, (N, C), dev)
+    shape = ConvStepShape(n_seq, N, state.shape[0], C, W, code, int(act), int(bool(update)), xs)
+    _run("sf_gdn_shortconv_step", dev, stream, ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(slots),
+         _ptr(seq_start), _ptr(state), _ptr(y))
+    return y
+
+
+def _heads(x):
+    """[N, H, D] view of x [..., H, D] (no copy)."""
+    if x.dim() < 3:
+        raise ValueError("expected [..., H, D], got shape %s" % (tuple(x.shape),))
+    return x if x.dim() == 3 else x.view(-1, x.shape[-2], x.shape[-1])
+
+
+def gated_norm_shape(x, gate=None, eps=1e-6, scale=1.0, act=1):
+    """GatedNormShape of x [N, H, D] and gate, which are checked."""
+    dev = _device_of(x, "x")
+    code = _dtype_code(x, "x")
+    N, H, D = x.shape
+    xs = _token_rows(x, "x", x.dtype, (N, H, D), dev)
+    gs = 0 if gate is None else _token_rows(gate, "gate", x.dtype, (N, H, D), dev)
+    return GatedNormShape(N, H, D, code, int(act), float(eps), float(scale), xs, gs)
+
+
+def gated_norm_bwd_workspace_bytes(shape):
+    n = ctypes.c_size_t(0)
+    _check(load().sf_gdn_gated_norm_bwd_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+           "gated_norm_bwd_workspace_size")
+    return n.value
+
+
+def gated_norm_fwd(x, gate=None, w=None, eps=1e-6, scale=1.0, act=1, y=None, stream=None):
+    """sf_gdn_gated_norm_fwd on torch tensors: y = scale * w * x / sqrt(mean(
+    x^2) + eps) * act(gate) over the last dimension of x [..., H, D], with
+    gate like x or None (factor 1) and w [D] fp32 or None (ones); act 1 for
+    SiLU, 0 for the gate itself.  x and gate may be head slices of wider token
+    rows."""
+    full = x.shape
+    x = _heads(x)
+    gate = None if gate is None else _heads(gate)
+    shape = gated_norm_shape(x, gate, eps, scale, act)
+    dev = x.device
+    if w is not None:
+        _need(w, "w", torch.float32, (x.shape[2],), dev)
+    if y is None:
+        y = torch.empty(full, dtype=x.dtype, device=dev)
+        used_on(stream, y)
+    _need(y, "y", x.dtype, full, dev)
+    _run("sf_gdn_gated_norm_fwd", dev, stream, ctypes.byref(shape), _ptr(x), _ptr(gate), _ptr(w),
+         _ptr(y))
+    return y
+
+
+def gated_norm_bwd(x, gate, w, dy, eps=1e-6, scale=1.0, act=1, grads=None, want_dw=True,
+                   workspace=None, stream=None):
+    """sf_gdn_gated_norm_bwd on torch tensors.  Returns (dx, dgate, dw), with
+    None for dgate without gate and for dw without w (or want_dw False).
+    ``grads`` may supply preallocated outputs in that order."""
+    full = x.shape
+    x = _heads(x)
+    gate = None if gate is None else _heads(gate)
+    shape = gated_norm_shape(x, gate, eps, scale, act)
+    dev, D = x.device, x.shape[2]
+    if w is not None:
+        _need(w, "w", torch.float32, (D,), dev)
+    _need(dy, "dy", x.dtype, full, dev)
+    want_dw = want_dw and w is not None
+    if grads is None:
+        grads = (torch.empty(full, dtype=x.dtype, device=dev),
+                 None if gate is None else torch.empty(full, dtype=x.dtype, device=dev),
+                 torch.empty(D, dtype=torch.float32, device=dev) if want_dw else None)
+        used_on(stream, *grads)
+    dx, dgate, dw = grads
+    _need(dx, "dx", x.dtype, full, dev)
+    if gate is not None:
+        _need(dgate, "dgate", x.dtype, full, dev)
+    elif dgate is not None:
+        raise ValueError("dgate without gate")
+    if want_dw:
+        _need(dw, "dw", torch.float32, (D,), dev)
+        need = gated_norm_bwd_workspace_bytes(shape)
+        if workspace is None or workspace.numel() < need:
+            workspace = alloc_workspace(need, dev)
+            used_on(stream, workspace)
+    else:
+        dw = workspace = None
+    wsn = ctypes.c_size_t(0 if workspace is None else workspace.numel())
+    _run("sf_gdn_gated_norm_bwd", dev, stream, ctypes.byref(shape), _ptr(x), _ptr(gate), _ptr(w),
+         _ptr(dy), _ptr(dx), _ptr(dgate), _ptr(dw), _ptr(workspace), wsn)
+    return dx, dgate, dw
+
+
+def residual_norm_shape(x, eps=1e-6, scale=1.0):
+    """ResidualNormShape of x [..., C]."""
+    C = x.shape[-1]
+    return ResidualNormShape(x.numel() // C if C else 0, C, _dtype_code(x, "x"), float(eps),
+                             float(scale))
+
+
+def residual_norm_bwd_workspace_bytes(shape):
+    n = ctypes.c_size_t(0)
+    _check(load().sf_gdn_residual_norm_bwd_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+           "residual_norm_bwd_workspace_size")
+    return n.value
+
+
+def residual_norm_fwd(x, r=None, w=None, s=None, scale=1.0, eps=1e-6, h=None, y=None,
+                      stream=None):
+    """sf_gdn_residual_norm_fwd on torch tensors: h = x + scale * s * r and
+    y = w * h / sqrt(mean(h^2) + eps) over the last dimension of x [..., C],
+    with r like x (None: h is x), s [C] fp32 (None: ones) and w [C] fp32
+    (None: ones).  Returns (y, h)."""
+    dev = _device_of(x, "x")
+    shape = residual_norm_shape(x, eps, scale)
+    _need(x, "x", x.dtype, x.shape, dev)
+    for t, n in ((w, "w"), (s, "s")):
+        if t is not None:
+            _need(t, n, torch.float32, (shape.C,), dev)
+    if r is not None:
+        _need(r, "r", x.dtype, x.shape, dev)
+        if h is None:
+            h = torch.empty_like(x)
+            used_on(stream, h)
+        _need(h, "h", x.dtype, x.shape, dev)
+    elif s is not None or h is not None:
+        raise ValueError("s and h need r")
+    if y is None:
+        y = torch.empty_like(x)
+        used_on(stream, y)
+    _need(y, "y", x.dtype, x.shape, dev)
+    _run("sf_gdn_residual_norm_fwd", dev, stream, ctypes.byref(shape), _ptr(x), _ptr(r), _ptr(s),
+         _ptr(w), _ptr(h), _ptr(y))
+    return y, (x if r is None else h)
+
+
+def residual_norm_bwd(h, r, w, s, dy, dh=None, scale=1.0, eps=1e-6, grads=None, want_dr=True,
+                      want_dw=True, want_ds=True, workspace=None, stream=None):
+    """sf_gdn_residual_norm_bwd on torch tensors: h as the forward returned
+    it, dy and dh (None: zeros) the gradients of y and h.  Returns (dx, dr, dw,
+    ds): dr is None with want_dr False, dw without w, ds without s (r is read
+    for ds only and may be None otherwise); ``grads`` may supply preallocated
+    outputs in that order."""
+    dev = _device_of(h, "h")
+    shape = residual_norm_shape(h, eps, scale)
+    C = shape.C
+    _need(h, "h", h.dtype, h.shape, dev)
+    _need(dy, "dy", h.dtype, h.shape, dev)
+    if dh is not None:
+        _need(dh, "dh", h.dtype, h.shape, dev)
+    for t, n in ((w, "w"), (s, "s")):
+        if t is not None:
+            _need(t, n, torch.float32, (C,), dev)
+    want_dw = want_dw and w is not None
+    want_ds = want_ds and s is not None
+    if want_ds:
+        _need(r, "r", h.dtype, h.shape, dev)
+    if grads is None:
+        grads = (torch.empty_like(h), torch.empty_like(h) if want_dr else None,
+                 torch.empty(C, dtype=torch.float32, device=dev) if want_dw else None,
+                 torch.empty(C, dtype=torch.float32, device=dev) if want_ds else None)
+        used_on(stream, *grads)
+    dx, dr, dw, ds = grads
+    _need(dx, "dx", h.dtype, h.shape, dev)
+    if want_dr:
+        _need(dr, "dr", h.dtype, h.shape, dev)
+    for t, n, want in ((dw, "dw", want_dw), (ds, "ds", want_ds)):
+        if want:
+            _need(t, n, torch.float32, (C,), dev)
+    need = 0
+    if want_dw or want_ds:
+        need = residual_norm_bwd_workspace_bytes(shape)
+        if workspace is None or workspace.numel() < need:
+            workspace = alloc_workspace(need, dev)
+            used_on(stream, workspace)
+    else:
+        workspace = None
+    wsn = ctypes.c_size_t(0 if workspace is None else workspace.numel())
+    _run("sf_gdn_residual_norm_bwd", dev, stream, ctypes.byref(shape), _ptr(h),
+         _ptr(r) if want_ds else None, _ptr(s), _ptr(w), _ptr(dy), _ptr(dh), _ptr(dx),
+         _ptr(dr) if want_dr else None, _ptr(dw) if want_dw else None,
+         _ptr(ds) if want_ds else None, _ptr(workspace), wsn)
+    return dx, (dr if want_dr else None), (dw if want_dw else None), (ds if want_ds else None)
 
 
 class profile:

@@ -2,6 +2,8 @@
 
     gated_delta_chunk(q, k, v, alpha, beta, S_in=None, seg_blocks=0) -> (o, S_out)
     short_conv(x, w, conv_in=None, act=0)                           -> (y, conv_out)
+    gated_norm(x, gate=None, w=None, eps, scale, act)               -> y
+    residual_norm(x, r=None, w=None, s=None, scale, eps)            -> (y, h)
 
 The forward is the saving forward (sf_gdn_chunk_fwd_save: o and S_out, with
 each block's entry state and V^new kept for the backward), and the backward is
@@ -11,10 +13,14 @@ chunk's boundary-state gradient dS_in ([SF] "What carries the argument",
 Eq. 7), so chunks chained through S_in = previous S_out differentiate as one
 sequence.  short_conv is the causal depthwise convolution ahead of the
 recurrence (sf_gdn_shortconv_fwd / _bwd), whose W-1-token boundary state
-chains the same way.  Argument marshalling only: both passes are the library's
+chains the same way.  gated_norm and residual_norm are the layer's norms after
+and before the recurrence (sf_gdn_gated_norm_*, sf_gdn_residual_norm_*); their
+backward keeps no statistics, it forms them again from x (h).  Argument
+marshalling only: both passes are the library's
 kernels, and CPU tensors are refused as in chunk_fwd.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 
@@ -73,3 +79,64 @@ def short_conv(x, w, conv_in=None, act=0):
     fp32, conv_in [B, W-1, C] in x's dtype or None (zeros, no gradient); act 0
     for none, 1 for SiLU."""
     return _ShortConv.apply(x, w, conv_in, act)
+
+
+def _aligned(g):
+    """A gradient as the library takes it: contiguous, from a 16-byte address."""
+    g = g.contiguous()
+    return g if g.data_ptr() % 16 == 0 else g.clone()
+
+
+class _GatedNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate, w, eps, scale, act):
+        y = _lib.gated_norm_fwd(x, gate, w, eps=eps, scale=scale, act=act)
+        ctx.save_for_backward(x, gate, w)
+        ctx.opts = dict(eps=eps, scale=scale, act=act)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, gate, w = ctx.saved_tensors
+        dx, dgate, dw = _lib.gated_norm_bwd(x, gate, w, _aligned(dy),
+                                            want_dw=ctx.needs_input_grad[2], **ctx.opts)
+        return dx, dgate, dw, None, None, None
+
+
+def gated_norm(x, gate=None, w=None, eps=1e-6, scale=1.0, act=1):
+    """y = scale * w * x / sqrt(mean(x^2) + eps) * act(gate) over the last
+    dimension of x [..., H, D], differentiable in x, gate and w; arguments as
+    in gated_norm_fwd."""
+    return _GatedNorm.apply(x, gate, w, eps, scale, act)
+
+
+class _ResidualNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, r, w, s, scale, eps):
+        y, h = _lib.residual_norm_fwd(x, r, w, s, scale=scale, eps=eps)
+        ctx.opts = dict(scale=scale, eps=eps)
+        ctx.has_r = r is not None
+        ctx.save_for_backward(h, r if s is not None else None, w, s)
+        return (y, h) if ctx.has_r else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dh=None):
+        h, r, w, s = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dr, dw, ds = _lib.residual_norm_bwd(
+            h, r, w, s, _aligned(dy), None if dh is None else _aligned(dh),
+            want_dr=ctx.has_r and need[1], want_dw=need[2], want_ds=need[3], **ctx.opts)
+        return dx, dr, dw, ds, None, None
+
+
+def residual_norm(x, r=None, w=None, s=None, scale=1.0, eps=1e-6):
+    """(y, h) with h = x + scale * s * r (x itself without r) and y = w * h /
+    sqrt(mean(h^2) + eps) over the last dimension, differentiable in x, r, w
+    and s; arguments as in residual_norm_fwd."""
+    if r is None:
+        if s is not None:
+            raise ValueError("s needs r")
+        return _ResidualNorm.apply(x, None, w, None, scale, eps), x
+    return _ResidualNorm.apply(x, r, w, s, scale, eps)

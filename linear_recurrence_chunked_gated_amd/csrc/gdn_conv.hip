@@ -14,7 +14,12 @@
 // The work is streaming (a few flops per element), so the kernels are laid
 // out for HBM: each thread walks a run of tokens for a few adjacent channels
 // with the W-1 previous inputs in registers, so every input is read once.
+//
+// This unit also compiles the other streaming kernels of a layer: the
+// single-token recurrence (gdn_step.hpp) and the norms (gdn_norm.hpp).
 #include "gdn_kernels.hpp"
+#include "gdn_norm.hpp"
+#include "gdn_step.hpp"
 
 namespace sfgdn {
 
@@ -294,6 +299,64 @@ __global__ __launch_bounds__(CONV_THREADS) void conv_dw_reduce_kernel(const floa
   out[(size_t)blockIdx.y * CW + i] = s;
 }
 
+// ------------------------------------------------- single tokens over a pool
+// Serving: every sequence of a batch brings its new tokens and finds its last
+// W-1 inputs in its slot of a state pool, updated in place.  Thread: V
+// channels, with their taps in registers over the sequences that its
+// workgroup column walks.
+constexpr int CONV_STEP_THREADS = 64;
+
+template <typename T, int W, int V>
+__global__ __launch_bounds__(CONV_STEP_THREADS) void conv_step_kernel(ConvStepArgs a) {
+  const int c = (blockIdx.x * CONV_STEP_THREADS + threadIdx.x) * V;
+  const bool live = c < a.C;
+  float wt[W][V];
+#pragma unroll
+  for (int j = 0; j < W; ++j)
+#pragma unroll
+    for (int i = 0; i < V; ++i) wt[j][i] = live ? a.w[(size_t)(c + i) * W + j] : 0.f;
+  for (int seq = blockIdx.y; seq < a.b.n_seq; seq += gridDim.y) {
+    const SeqEntry e = seq_entry(a.b, seq);
+    if (e.slot < 0 || e.t0 >= e.t1) continue;
+    const bool bad = e.bad || (a.update && a.b.slots && slot_repeats(a.b, seq, e.slot));
+    if (!live) continue;
+    T* __restrict__ y = reinterpret_cast<T*>(a.y) + c;
+    if (bad) {
+      float nan[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) nan[i] = __builtin_nanf("");
+      for (int t = e.t0; t < e.t1; ++t) st_vec<T, V>(y + (size_t)t * a.C, nan);
+      continue;
+    }
+    const T* __restrict__ x = reinterpret_cast<const T*>(a.x) + c;
+    T* state = reinterpret_cast<T*>(a.state) + (size_t)e.slot * (W - 1) * a.C + c;
+    float win[W][V];  // win[j] = the input j tokens before the current one
+#pragma unroll
+    for (int j = 1; j < W; ++j) ld_vec<T, V>(state + (size_t)(W - 1 - j) * a.C, win[j]);
+#pragma unroll 4
+    for (int t = e.t0; t < e.t1; ++t) {
+      ld_vec<T, V>(x + (size_t)t * a.xs, win[0]);
+      float z[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) s += wt[j][i] * win[j][i];
+        z[i] = a.act ? silu(s) : s;
+      }
+      st_vec<T, V>(y + (size_t)t * a.C, z);
+#pragma unroll
+      for (int j = W - 1; j >= 1; --j)
+#pragma unroll
+        for (int i = 0; i < V; ++i) win[j][i] = win[j - 1][i];
+    }
+    if (a.update) {
+#pragma unroll
+      for (int j = 1; j < W; ++j) st_vec<T, V>(state + (size_t)(W - 1 - j) * a.C, win[j]);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ launch
 template <typename T> constexpr int conv_vf() { return 16 / sizeof(T); }  // fwd channels/thread
 template <typename T> constexpr int conv_vb() { return 8 / sizeof(T); }   // bwd channels/thread
@@ -380,9 +443,37 @@ hipError_t launch_conv_bwd(const ConvArgs& a, int GR, float* dwp, hipStream_t st
   return hipErrorInvalidValue;
 }
 
+template <typename T, int W>
+static hipError_t conv_step_w(const ConvStepArgs& a, hipStream_t st, Profiler* prof) {
+  constexpr int V = conv_vf<T>();
+  const int gx = (a.C / V + CONV_STEP_THREADS - 1) / CONV_STEP_THREADS;
+  prof_begin(prof, "conv_step", st);
+  hipLaunchKernelGGL((conv_step_kernel<T, W, V>), dim3(gx, a.b.n_seq < 65535 ? a.b.n_seq : 65535),
+                     dim3(CONV_STEP_THREADS), 0, st, a);
+  prof_end(prof, st);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t launch_conv_step(const ConvStepArgs& a, hipStream_t st, Profiler* prof) {
+  switch (a.W) {
+    case 1: return conv_step_w<T, 1>(a, st, prof);
+    case 2: return conv_step_w<T, 2>(a, st, prof);
+    case 3: return conv_step_w<T, 3>(a, st, prof);
+    case 4: return conv_step_w<T, 4>(a, st, prof);
+    case 5: return conv_step_w<T, 5>(a, st, prof);
+    case 6: return conv_step_w<T, 6>(a, st, prof);
+    case 7: return conv_step_w<T, 7>(a, st, prof);
+    case 8: return conv_step_w<T, 8>(a, st, prof);
+  }
+  return hipErrorInvalidValue;
+}
+
 template hipError_t launch_conv_fwd<bf16>(const ConvArgs&, hipStream_t, Profiler*);
 template hipError_t launch_conv_fwd<float>(const ConvArgs&, hipStream_t, Profiler*);
 template hipError_t launch_conv_bwd<bf16>(const ConvArgs&, int, float*, hipStream_t, Profiler*);
 template hipError_t launch_conv_bwd<float>(const ConvArgs&, int, float*, hipStream_t, Profiler*);
+template hipError_t launch_conv_step<bf16>(const ConvStepArgs&, hipStream_t, Profiler*);
+template hipError_t launch_conv_step<float>(const ConvStepArgs&, hipStream_t, Profiler*);
 
 }  // namespace sfgdn

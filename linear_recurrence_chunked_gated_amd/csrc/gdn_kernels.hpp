@@ -102,6 +102,87 @@ struct ConvArgs {
   int B, T, C, W, act;
 };
 
+// A batch of sequences over a pool of per-sequence states: entry i's slot in
+// the pool (null: slot i) and its token rows seq_start[i] .. seq_start[i+1]-1
+// (null: `uniform` rows each).  Both arrays live on the device.
+struct PoolBatch {
+  const int* slots;
+  const int* seq_start;
+  int n_seq, n_tok, n_slots, uniform;
+};
+
+// The recurrence by single tokens (see gdn_step.hpp).  q, k [n_tok, Hk, D],
+// v [n_tok, Hv, D] with qs, ks, vs elements between token rows; alpha, beta
+// [n_tok, Hv]; state [n_slots, Hv, D, D]; o [n_tok, Hv, D].
+struct StepArgs {
+  PoolBatch b;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* alpha;
+  const float* beta;
+  float* state;
+  void* o;
+  long long qs, ks, vs;
+  int Hv, group;  // group = Hv / Hk value heads share a key head
+  int update;     // write the exit states
+};
+
+// The short convolution by single tokens (see gdn_conv.hip): x [n_tok, C]
+// with xs elements between rows, state [n_slots, W-1, C], y [n_tok, C].
+struct ConvStepArgs {
+  PoolBatch b;
+  const void* x;
+  const float* w;
+  void* state;
+  void* y;
+  long long xs;
+  int C, W, act, update;
+};
+
+// Per-head norm with its gate (see gdn_norm.hpp): N tokens of H heads of D
+// values; xs and gs elements between token rows of x and gate, the other
+// tensors contiguous.  Null gate: factor 1.  Null w: ones.
+struct GatedNormArgs {
+  const void* x;
+  const void* gate;
+  const float* w;
+  void* y;
+  const void* dy;
+  void* dx;
+  void* dgate;
+  float* part;  // backward with w: [groups][D] partial weight gradients
+  float* dw;
+  long long N, xs, gs;
+  int H, D, act;
+  float eps, scale;
+};
+
+// Residual sum and norm (see gdn_norm.hpp): N rows of C values, contiguous.
+// Null r: h is x and is not written.  Null s: ones.  Null w: ones.
+struct ResidualNormArgs {
+  const void* x;  // forward: x; backward: h
+  const void* r;
+  const float* w;
+  const float* s;
+  void* h;
+  void* y;
+  const void* dy;
+  const void* dh;  // may be null (zeros)
+  void* dx;
+  void* dr;
+  float* part;  // backward: [groups][C] per weight gradient wanted (dw, then ds)
+  float* dw;
+  float* ds;
+  long long N;
+  int C;
+  float eps, scale;
+};
+// Workgroups of the backward kernels, each with one row of partial weight
+// gradients: fixed by the shape, so that the sums' order is too.
+int gated_norm_groups(long long N, int H, int D);
+int residual_norm_groups(long long N, int C);
+
 // Optional per-launch event timing (see sf_gdn_profile_* in the C ABI).
 struct Profiler;
 void prof_begin(Profiler* p, const char* name, hipStream_t st);
@@ -140,5 +221,19 @@ template <typename T>
 hipError_t launch_conv_fwd(const ConvArgs& a, hipStream_t st, Profiler* prof);
 template <typename T>
 hipError_t launch_conv_bwd(const ConvArgs& a, int GR, float* dwp, hipStream_t st, Profiler* prof);
+// Single-token forms over a pool of states.
+template <typename T, int D>
+hipError_t launch_recurrent_step(const StepArgs& a, hipStream_t st, Profiler* prof);
+template <typename T>
+hipError_t launch_conv_step(const ConvStepArgs& a, hipStream_t st, Profiler* prof);
+// Norms.
+template <typename T>
+hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, hipStream_t st, Profiler* prof);
+template <typename T>
+hipError_t launch_gated_norm_bwd(const GatedNormArgs& a, hipStream_t st, Profiler* prof);
+template <typename T>
+hipError_t launch_residual_norm_fwd(const ResidualNormArgs& a, hipStream_t st, Profiler* prof);
+template <typename T>
+hipError_t launch_residual_norm_bwd(const ResidualNormArgs& a, hipStream_t st, Profiler* prof);
 
 }  // namespace sfgdn

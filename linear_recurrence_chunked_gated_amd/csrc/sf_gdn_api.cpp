@@ -787,3 +787,343 @@ sf_status sf_gdn_shortconv_bwd(const sf_conv_shape* shape, const void* x, const 
 }
 
 }  // extern "C"
+
+// ------------------------------------------------ single tokens over a pool
+namespace {
+
+sf_status check_ints(const int* p, const char* name) {
+  if ((uintptr_t)p % 4) return fail(SF_ERR_INVALID_ARG, std::string(name) + " is not 4-byte aligned");
+  return SF_OK;
+}
+
+// Outputs against small inputs that need only 4-byte alignment.
+sf_status check_apart(const std::vector<Range>& in, const std::vector<Range>& out) {
+  for (const Range& o : out)
+    for (const Range& r : in)
+      if (overlap(o, r))
+        return fail(SF_ERR_INVALID_ARG, std::string(o.name) + " overlaps input " + r.name);
+  return SF_OK;
+}
+
+// The pool batch of a step call; *stride of a token tensor: 0 means `width`.
+sf_status make_batch(int n_seq, int n_tok, int n_slots, const int* slots, const int* seq_start,
+                     PoolBatch& b) {
+  if (n_seq < 0 || n_tok < 0 || n_slots < 0)
+    return fail(SF_ERR_INVALID_ARG, "n_seq, n_tok and n_slots must be >= 0");
+  if (!slots && n_slots < n_seq)
+    return fail(SF_ERR_INVALID_ARG, "without slots the pool needs a slot per sequence");
+  if (!seq_start && n_seq > 0 && n_tok % n_seq)
+    return fail(SF_ERR_INVALID_ARG, "without seq_start n_tok must be a multiple of n_seq");
+  if (!seq_start && n_seq == 0 && n_tok > 0)
+    return fail(SF_ERR_INVALID_ARG, "tokens without a sequence");
+  sf_status s;
+  if ((s = check_ints(slots, "slots")) != SF_OK) return s;
+  if ((s = check_ints(seq_start, "seq_start")) != SF_OK) return s;
+  b.slots = slots;
+  b.seq_start = seq_start;
+  b.n_seq = n_seq;
+  b.n_tok = n_tok;
+  b.n_slots = n_slots;
+  b.uniform = n_seq > 0 ? n_tok / n_seq : 0;
+  return SF_OK;
+}
+
+sf_status token_stride(long long given, long long width, const char* name, long long* out) {
+  if (given == 0) given = width;
+  if (given < width || given % 8 || given > (1LL << 31))
+    return fail(SF_ERR_INVALID_ARG, std::string(name) + " stride must be a multiple of 8 elements, at least a row");
+  *out = given;
+  return SF_OK;
+}
+
+// bytes that a strided token tensor spans
+size_t span(long long rows, long long stride, long long width, size_t es) {
+  return rows > 0 ? (size_t)((rows - 1) * stride + width) * es : 0;
+}
+
+sf_status check_dtype(int dtype) {
+  if (dtype != SF_DTYPE_F32 && dtype != SF_DTYPE_BF16)
+    return fail(SF_ERR_INVALID_ARG, "unknown dtype");
+  return SF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sf_status sf_gdn_recurrent_step(const sf_step_shape* shape, const void* q, const void* k,
+                                const void* v, const float* alpha, const float* beta,
+                                const int* slots, const int* seq_start, float* state, void* o,
+                                void* stream) {
+  if (!shape) return fail(SF_ERR_INVALID_ARG, "shape is NULL");
+  const sf_step_shape& p = *shape;
+  sf_status s;
+  StepArgs a{};
+  if ((s = check_dtype(p.dtype)) != SF_OK) return s;
+  if (p.Hk <= 0 || p.Hv <= 0 || p.Dk <= 0 || p.Dv <= 0)
+    return fail(SF_ERR_INVALID_ARG, "Hk, Hv, Dk and Dv must be positive");
+  if (p.Hv % p.Hk) return fail(SF_ERR_INVALID_ARG, "Hv must be a multiple of Hk");
+  if (p.Dk != p.Dv || (p.Dk != 64 && p.Dk != 128))
+    return fail(SF_ERR_UNSUPPORTED, "Dk == Dv in {64, 128} supported");
+  if (p.update != 0 && p.update != 1) return fail(SF_ERR_INVALID_ARG, "update must be 0 or 1");
+  // one workgroup takes at least 32 rows of a state; a launch holds 2^32 threads
+  if (p.Hv > (1 << 16) || (long long)p.n_seq * p.Hv > (1LL << 21))
+    return fail(SF_ERR_UNSUPPORTED, "n_seq * Hv too large");
+  if ((s = make_batch(p.n_seq, p.n_tok, p.n_slots, slots, seq_start, a.b)) != SF_OK) return s;
+  const int D = p.Dk;
+  if ((s = token_stride(p.q_stride, (long long)p.Hk * D, "q", &a.qs)) != SF_OK) return s;
+  if ((s = token_stride(p.k_stride, (long long)p.Hk * D, "k", &a.ks)) != SF_OK) return s;
+  if ((s = token_stride(p.v_stride, (long long)p.Hv * D, "v", &a.vs)) != SF_OK) return s;
+  if (p.n_seq == 0 || p.n_tok == 0) return SF_OK;
+  if (!q || !k || !v || !alpha || !beta || !state || !o)
+    return fail(SF_ERR_INVALID_ARG, "q, k, v, alpha, beta, state and o are required");
+  const size_t es = p.dtype == SF_DTYPE_BF16 ? 2 : 4;
+  const size_t gates = (size_t)p.n_tok * p.Hv * 4;
+  std::vector<Range> in = {{q, span(p.n_tok, a.qs, (long long)p.Hk * D, es), "q"},
+                           {k, span(p.n_tok, a.ks, (long long)p.Hk * D, es), "k"},
+                           {v, span(p.n_tok, a.vs, (long long)p.Hv * D, es), "v"}};
+  std::vector<Range> out = {{state, (size_t)p.n_slots * p.Hv * D * D * 4, "state"},
+                            {o, (size_t)p.n_tok * p.Hv * D * es, "o"}};
+  std::vector<Range> small = {{alpha, gates, "alpha"}, {beta, gates, "beta"},
+                              {slots, (size_t)p.n_seq * 4, "slots"},
+                              {seq_start, ((size_t)p.n_seq + 1) * 4, "seq_start"}};
+  if ((s = check_ptrs(in, out, {})) != SF_OK) return s;
+  if ((s = check_apart(small, out)) != SF_OK) return s;
+  if (((uintptr_t)alpha | (uintptr_t)beta) % 4)
+    return fail(SF_ERR_INVALID_ARG, "alpha and beta must be 4-byte aligned");
+  a.q = q; a.k = k; a.v = v; a.alpha = alpha; a.beta = beta; a.state = state; a.o = o;
+  a.Hv = p.Hv; a.group = p.Hv / p.Hk; a.update = p.update;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e;
+    if (p.dtype == SF_DTYPE_BF16)
+      e = D == 64 ? launch_recurrent_step<bf16, 64>(a, st, prof)
+                  : launch_recurrent_step<bf16, 128>(a, st, prof);
+    else
+      e = D == 64 ? launch_recurrent_step<float, 64>(a, st, prof)
+                  : launch_recurrent_step<float, 128>(a, st, prof);
+    if (e != hipSuccess) return hip_fail(e, "recurrent step launch");
+    return SF_OK;
+  });
+}
+
+sf_status sf_gdn_shortconv_step(const sf_conv_step_shape* shape, const void* x, const float* w,
+                                const int* slots, const int* seq_start, void* state, void* y,
+                                void* stream) {
+  if (!shape) return fail(SF_ERR_INVALID_ARG, "shape is NULL");
+  const sf_conv_step_shape& p = *shape;
+  sf_status s;
+  ConvStepArgs a{};
+  if ((s = check_dtype(p.dtype)) != SF_OK) return s;
+  if (p.C <= 0) return fail(SF_ERR_INVALID_ARG, "C must be positive");
+  if (p.W < 1 || p.W > 8) return fail(SF_ERR_UNSUPPORTED, "W must be in 1..8");
+  if (p.act != 0 && p.act != 1) return fail(SF_ERR_INVALID_ARG, "act must be 0 or 1");
+  if (p.update != 0 && p.update != 1) return fail(SF_ERR_INVALID_ARG, "update must be 0 or 1");
+  if (p.C % 8 || p.C > (1 << 24)) return fail(SF_ERR_UNSUPPORTED, "C must be a multiple of 8, at most 2^24");
+  if ((s = make_batch(p.n_seq, p.n_tok, p.n_slots, slots, seq_start, a.b)) != SF_OK) return s;
+  if ((s = token_stride(p.x_stride, p.C, "x", &a.xs)) != SF_OK) return s;
+  if (p.n_seq == 0 || p.n_tok == 0) return SF_OK;
+  if (!x || !w || !y || (p.W > 1 && !state))
+    return fail(SF_ERR_INVALID_ARG, "x, w, state and y are required");
+  const size_t es = p.dtype == SF_DTYPE_BF16 ? 2 : 4;
+  std::vector<Range> in = {{x, span(p.n_tok, a.xs, p.C, es), "x"},
+                           {w, (size_t)p.C * p.W * 4, "w"}};
+  std::vector<Range> out = {{state, (size_t)p.n_slots * (p.W - 1) * p.C * es, "state"},
+                            {y, (size_t)p.n_tok * p.C * es, "y"}};
+  std::vector<Range> small = {{slots, (size_t)p.n_seq * 4, "slots"},
+                              {seq_start, ((size_t)p.n_seq + 1) * 4, "seq_start"}};
+  if ((s = check_ptrs(in, out, {})) != SF_OK) return s;
+  if ((s = check_apart(small, out)) != SF_OK) return s;
+  a.x = x; a.w = w; a.state = state; a.y = y;
+  a.C = p.C; a.W = p.W; a.act = p.act; a.update = p.update;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e = p.dtype == SF_DTYPE_BF16 ? launch_conv_step<bf16>(a, st, prof)
+                                           : launch_conv_step<float>(a, st, prof);
+    if (e != hipSuccess) return hip_fail(e, "convolution step launch");
+    return SF_OK;
+  });
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------- norms
+namespace {
+
+sf_status make_gated(const sf_gated_norm_shape* p, GatedNormArgs& a) {
+  sf_status s;
+  if (!p) return fail(SF_ERR_INVALID_ARG, "shape is NULL");
+  if ((s = check_dtype(p->dtype)) != SF_OK) return s;
+  if (p->N < 0 || p->H <= 0 || p->D <= 0)
+    return fail(SF_ERR_INVALID_ARG, "H and D must be positive and N >= 0");
+  if (p->D % 8 || p->D > 512)
+    return fail(SF_ERR_UNSUPPORTED, "D must be a multiple of 8, at most 512");
+  if (p->act != 0 && p->act != 1) return fail(SF_ERR_INVALID_ARG, "act must be 0 or 1");
+  if (!(p->eps >= 0.f)) return fail(SF_ERR_INVALID_ARG, "eps must be >= 0");
+  if (p->N > (1LL << 40) / p->H || p->N * p->H > (1LL << 40) / p->D)
+    return fail(SF_ERR_UNSUPPORTED, "too large");
+  const long long row = (long long)p->H * p->D;
+  if ((s = token_stride(p->x_stride, row, "x", &a.xs)) != SF_OK) return s;
+  if ((s = token_stride(p->gate_stride, row, "gate", &a.gs)) != SF_OK) return s;
+  a.N = p->N; a.H = p->H; a.D = p->D; a.act = p->act; a.eps = p->eps; a.scale = p->scale;
+  return SF_OK;
+}
+
+sf_status make_residual(const sf_residual_norm_shape* p, ResidualNormArgs& a) {
+  sf_status s;
+  if (!p) return fail(SF_ERR_INVALID_ARG, "shape is NULL");
+  if ((s = check_dtype(p->dtype)) != SF_OK) return s;
+  if (p->N < 0 || p->C <= 0) return fail(SF_ERR_INVALID_ARG, "C must be positive and N >= 0");
+  if (p->C % 8 || p->C > 16384)
+    return fail(SF_ERR_UNSUPPORTED, "C must be a multiple of 8, at most 16384");
+  if (!(p->eps >= 0.f)) return fail(SF_ERR_INVALID_ARG, "eps must be >= 0");
+  if (p->N > (1LL << 40) / p->C) return fail(SF_ERR_UNSUPPORTED, "too large");
+  a.N = p->N; a.C = p->C; a.eps = p->eps; a.scale = p->scale;
+  return SF_OK;
+}
+
+size_t es_of(int dtype) { return dtype == SF_DTYPE_BF16 ? 2 : 4; }
+
+sf_status check_norm_ws(size_t need, const void* workspace, size_t ws_bytes) {
+  if (need > 0 && (!workspace || ws_bytes < need))
+    return fail(SF_ERR_WORKSPACE, "norm backward workspace needs " + std::to_string(need) + " bytes");
+  if (workspace && ((uintptr_t)workspace % kAlign))
+    return fail(SF_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  return SF_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sf_status sf_gdn_gated_norm_fwd(const sf_gated_norm_shape* shape, const void* x, const void* gate,
+                                const float* w, void* y, void* stream) {
+  GatedNormArgs a{};
+  sf_status s = make_gated(shape, a);
+  if (s != SF_OK) return s;
+  if (a.N == 0) return SF_OK;
+  if (!x || !y) return fail(SF_ERR_INVALID_ARG, "x and y are required");
+  const size_t es = es_of(shape->dtype);
+  const long long row = (long long)a.H * a.D;
+  std::vector<Range> in = {{x, span(a.N, a.xs, row, es), "x"},
+                           {gate, span(a.N, a.gs, row, es), "gate"},
+                           {w, (size_t)a.D * 4, "w"}};
+  std::vector<Range> out = {{y, (size_t)(a.N * row) * es, "y"}};
+  if ((s = check_ptrs(in, out, {})) != SF_OK) return s;
+  a.x = x; a.gate = gate; a.w = w; a.y = y;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e = shape->dtype == SF_DTYPE_BF16 ? launch_gated_norm_fwd<bf16>(a, st, prof)
+                                                : launch_gated_norm_fwd<float>(a, st, prof);
+    if (e != hipSuccess) return hip_fail(e, "gated norm launch");
+    return SF_OK;
+  });
+}
+
+sf_status sf_gdn_gated_norm_bwd_workspace_size(const sf_gated_norm_shape* shape, size_t* bytes) {
+  GatedNormArgs a{};
+  sf_status s = make_gated(shape, a);
+  if (s != SF_OK) return s;
+  if (!bytes) return fail(SF_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = align_up((size_t)gated_norm_groups(a.N, a.H, a.D) * a.D * 4);
+  return SF_OK;
+}
+
+sf_status sf_gdn_gated_norm_bwd(const sf_gated_norm_shape* shape, const void* x, const void* gate,
+                                const float* w, const void* dy, void* dx, void* dgate, float* dw,
+                                void* workspace, size_t ws_bytes, void* stream) {
+  GatedNormArgs a{};
+  sf_status s = make_gated(shape, a);
+  if (s != SF_OK) return s;
+  if (a.N > 0 && (!x || !dy || !dx)) return fail(SF_ERR_INVALID_ARG, "x, dy and dx are required");
+  if (a.N > 0 && !gate != !dgate)
+    return fail(SF_ERR_INVALID_ARG, "gate and dgate come together");
+  if (dw && !w) return fail(SF_ERR_INVALID_ARG, "dw needs w");
+  const size_t es = es_of(shape->dtype);
+  const long long row = (long long)a.H * a.D;
+  const size_t flat = (size_t)(a.N * row) * es;
+  std::vector<Range> in = {{x, span(a.N, a.xs, row, es), "x"},
+                           {gate, span(a.N, a.gs, row, es), "gate"},
+                           {w, (size_t)a.D * 4, "w"}, {dy, flat, "dy"},
+                           {workspace, ws_bytes, "workspace"}};
+  std::vector<Range> out = {{dx, flat, "dx"}, {dgate, flat, "dgate"}, {dw, (size_t)a.D * 4, "dw"}};
+  if ((s = check_ptrs(in, out, {})) != SF_OK) return s;
+  const size_t need =
+      dw ? align_up((size_t)gated_norm_groups(a.N, a.H, a.D) * a.D * 4) : 0;
+  if ((s = check_norm_ws(need, workspace, ws_bytes)) != SF_OK) return s;
+  a.x = x; a.gate = gate; a.w = w; a.dy = dy; a.dx = dx; a.dgate = dgate; a.dw = dw;
+  a.part = dw ? (float*)workspace : nullptr;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e = shape->dtype == SF_DTYPE_BF16 ? launch_gated_norm_bwd<bf16>(a, st, prof)
+                                                : launch_gated_norm_bwd<float>(a, st, prof);
+    if (e != hipSuccess) return hip_fail(e, "gated norm launch");
+    return SF_OK;
+  });
+}
+
+sf_status sf_gdn_residual_norm_fwd(const sf_residual_norm_shape* shape, const void* x,
+                                   const void* r, const float* s, const float* w, void* h, void* y,
+                                   void* stream) {
+  ResidualNormArgs a{};
+  sf_status st_ = make_residual(shape, a);
+  if (st_ != SF_OK) return st_;
+  if (a.N == 0) return SF_OK;
+  if (!x || !y) return fail(SF_ERR_INVALID_ARG, "x and y are required");
+  if (!r != !h) return fail(SF_ERR_INVALID_ARG, "r and h come together");
+  if (s && !r) return fail(SF_ERR_INVALID_ARG, "s needs r");
+  const size_t n = (size_t)(a.N * a.C) * es_of(shape->dtype), vec = (size_t)a.C * 4;
+  std::vector<Range> in = {{x, n, "x"}, {r, n, "r"}, {s, vec, "s"}, {w, vec, "w"}};
+  std::vector<Range> out = {{h, n, "h"}, {y, n, "y"}};
+  if ((st_ = check_ptrs(in, out, {})) != SF_OK) return st_;
+  a.x = x; a.r = r; a.s = s; a.w = w; a.h = h; a.y = y;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e = shape->dtype == SF_DTYPE_BF16 ? launch_residual_norm_fwd<bf16>(a, st, prof)
+                                                : launch_residual_norm_fwd<float>(a, st, prof);
+    if (e != hipSuccess) return hip_fail(e, "residual norm launch");
+    return SF_OK;
+  });
+}
+
+sf_status sf_gdn_residual_norm_bwd_workspace_size(const sf_residual_norm_shape* shape,
+                                                  size_t* bytes) {
+  ResidualNormArgs a{};
+  sf_status s = make_residual(shape, a);
+  if (s != SF_OK) return s;
+  if (!bytes) return fail(SF_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = align_up((size_t)residual_norm_groups(a.N, a.C) * a.C * 4 * 2);
+  return SF_OK;
+}
+
+sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const void* h,
+                                   const void* r, const float* s, const float* w, const void* dy,
+                                   const void* dh, void* dx, void* dr, float* dw, float* ds,
+                                   void* workspace, size_t ws_bytes, void* stream) {
+  ResidualNormArgs a{};
+  sf_status st_ = make_residual(shape, a);
+  if (st_ != SF_OK) return st_;
+  if (a.N > 0 && (!h || !dy || !dx)) return fail(SF_ERR_INVALID_ARG, "h, dy and dx are required");
+  if (dw && !w) return fail(SF_ERR_INVALID_ARG, "dw needs w");
+  if (ds && (!s || (a.N > 0 && !r))) return fail(SF_ERR_INVALID_ARG, "ds needs s and r");
+  const size_t n = (size_t)(a.N * a.C) * es_of(shape->dtype), vec = (size_t)a.C * 4;
+  std::vector<Range> in = {{h, n, "h"}, {r, n, "r"}, {s, vec, "s"}, {w, vec, "w"}, {dy, n, "dy"},
+                           {dh, n, "dh"}, {workspace, ws_bytes, "workspace"}};
+  std::vector<Range> out = {{dx, n, "dx"}, {dr, n, "dr"}, {dw, vec, "dw"}, {ds, vec, "ds"}};
+  if ((st_ = check_ptrs(in, out, {})) != SF_OK) return st_;
+  const size_t need = align_up((size_t)residual_norm_groups(a.N, a.C) * a.C * 4 *
+                               ((dw ? 1 : 0) + (ds ? 1 : 0)));
+  if ((st_ = check_norm_ws(need, workspace, ws_bytes)) != SF_OK) return st_;
+  a.x = h; a.r = r; a.s = s; a.w = w; a.dy = dy; a.dh = dh; a.dx = dx; a.dr = dr; a.dw = dw;
+  a.ds = ds;
+  a.part = (float*)workspace;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e = shape->dtype == SF_DTYPE_BF16 ? launch_residual_norm_bwd<bf16>(a, st, prof)
+                                                : launch_residual_norm_bwd<float>(a, st, prof);
+    if (e != hipSuccess) return hip_fail(e, "residual norm launch");
+    return SF_OK;
+  });
+}
+
+}  // extern "C"
