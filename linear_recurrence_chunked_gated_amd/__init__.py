@@ -26,15 +26,13 @@ __all__ = ["chunk_fwd", "chunk_bwd", "chain_fwd", "chain_bwd", "gated_delta_chun
 
 
 def __getattr__(name):
-    if name in ("chunk_fwd", "chunk_bwd", "shortconv_fwd", "shortconv_bwd", "recurrent_step",
-                "shortconv_step", "gated_norm_fwd", "gated_norm_bwd", "residual_norm_fwd",
-                "residual_norm_bwd", "profile", "GDNError"):
-        from . import _lib
-        return getattr(_lib, name)
     if name in ("chain_fwd", "chain_bwd"):
-        from . import chain
-        return getattr(chain, name)
-    if name in ("gated_delta_chunk", "short_conv", "gated_norm", "residual_norm"):
-        from . import autograd
-        return getattr(autograd, name)
-    raise AttributeError(name)
+        from . import chain as module
+    elif name in ("gated_delta_chunk", "short_conv", "gated_norm", "residual_norm"):
+        from . import autograd as module
+    elif name in __all__:
+        from . import _lib as module
+    else:
+        raise AttributeError(name)
+    globals()[name] = value = getattr(module, name)  # the next look-up finds it in the module
+    return value

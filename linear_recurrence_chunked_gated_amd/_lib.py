@@ -5,6 +5,7 @@ every step of the computation runs in the library's HIP kernels.  There is no
 fallback: if the library is missing or fails, calls raise.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -196,6 +197,9 @@ def alloc_workspace(nbytes, device):
 
 
 def _need(t, name, dtype, shape, device):
+    if (t is not None and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return
     if t is None:
         raise ValueError("%s is required" % name)
     if t.device != device:
@@ -453,25 +457,42 @@ def _device_of(t, name):
     return t.device
 
 
-def _run(name, dev, stream, *args):
-    """The call `name` on `stream` (the current stream of `dev` when None),
-    with `dev` current, so that tensors of another device than the current one
-    run on their own."""
-    if stream is not None and stream.device != dev:
+@functools.lru_cache(maxsize=4096)
+def _shape_ref(cls, *fields):
+    """A shape structure, as the calls take it (they only read it)."""
+    return ctypes.byref(cls(*fields))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(fn, dev, stream, *args):
+    """The call `fn` on `stream` (the current stream of `dev` when None), with
+    `dev` current, so that tensors of another device than the current one run
+    on their own."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif stream.device != dev:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
-    fn = getattr(load(), name)
+    else:
+        raw = stream.cuda_stream
+    call = getattr(_lib or load(), fn)
     if torch.cuda.current_device() == dev.index:
-        st = fn(*args, _stream(stream))
+        st = call(*args, raw)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(stream))
-    _check(st, name)
+            st = call(*args, raw)
+    if st != SF_OK:
+        _check(st, fn)
 
 
 def _token_rows(t, name, dtype, shape, device):
     """Elements between the token rows of t [n, ...], whose rows are
     contiguous but may lie apart (a slice of wider rows); 0 when there is at
     most one."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return 0
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
     if t.dtype != dtype:
@@ -480,13 +501,16 @@ def _token_rows(t, name, dtype, shape, device):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     if t.is_contiguous() or t.shape[0] == 0:
         return 0
-    if not t[0].is_contiguous():
-        raise ValueError("%s: each token's row must be contiguous" % name)
+    strides, width = t.stride(), 1
+    for n, st in zip(reversed(t.shape[1:]), reversed(strides[1:])):
+        if n != 1 and st != width:
+            raise ValueError("%s: each token's row must be contiguous" % name)
+        width *= n
     if t.shape[0] == 1:
         return 0
-    if t.stride(0) < t[0].numel():
+    if strides[0] < width:
         raise ValueError("%s: token rows must not overlap" % name)
-    return t.stride(0)
+    return strides[0]
 
 
 def _dtype_code(t, name):
@@ -537,10 +561,11 @@ def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=No
         o = torch.empty((N, Hv, Dv), dtype=q.dtype, device=dev)
         used_on(stream, o)
     _need(o, "o", q.dtype, (N, Hv, Dv), dev)
-    shape = StepShape(n_seq, N, state.shape[0], Hk, Hv, Dk, Dv, code, int(bool(update)), qs, ks,
-                      vs)
-    _run("sf_gdn_recurrent_step", dev, stream, ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
-         _ptr(alpha), _ptr(beta), _ptr(slots), _ptr(seq_start), _ptr(state), _ptr(o))
+    shape = _shape_ref(StepShape, n_seq, N, state.shape[0], Hk, Hv, Dk, Dv, code,
+                       1 if update else 0, qs, ks, vs)
+    _run("sf_gdn_recurrent_step", dev, stream, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+         alpha.data_ptr(), beta.data_ptr(), _addr(slots), _addr(seq_start), state.data_ptr(),
+         o.data_ptr())
     return o
 
 
@@ -566,9 +591,10 @@ def shortconv_step(x, w, state, slots=None, seq_start=None, act=0, y=None, updat
         y = torch.empty((N, C), dtype=x.dtype, device=dev)
         used_on(stream, y)
     _need(y, "y", x.dtype, (N, C), dev)
-    shape = ConvStepShape(n_seq, N, state.shape[0], C, W, code, int(act), int(bool(update)), xs)
-    _run("sf_gdn_shortconv_step", dev, stream, ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(slots),
-         _ptr(seq_start), _ptr(state), _ptr(y))
+    shape = _shape_ref(ConvStepShape, n_seq, N, state.shape[0], C, W, code, int(act),
+                       1 if update else 0, xs)
+    _run("sf_gdn_shortconv_step", dev, stream, shape, x.data_ptr(), w.data_ptr(), _addr(slots),
+         _addr(seq_start), state.data_ptr(), y.data_ptr())
     return y
 
 
@@ -580,18 +606,20 @@ def _heads(x):
 
 
 def gated_norm_shape(x, gate=None, eps=1e-6, scale=1.0, act=1):
-    """GatedNormShape of x [N, H, D] and gate, which are checked."""
+    """GatedNormShape of x [N, H, D] and gate, which are checked, by
+    reference."""
     dev = _device_of(x, "x")
     code = _dtype_code(x, "x")
-    N, H, D = x.shape
-    xs = _token_rows(x, "x", x.dtype, (N, H, D), dev)
-    gs = 0 if gate is None else _token_rows(gate, "gate", x.dtype, (N, H, D), dev)
-    return GatedNormShape(N, H, D, code, int(act), float(eps), float(scale), xs, gs)
+    full = N, H, D = x.shape
+    xs = _token_rows(x, "x", x.dtype, full, dev)
+    gs = 0 if gate is None else _token_rows(gate, "gate", x.dtype, full, dev)
+    return _shape_ref(GatedNormShape, N, H, D, code, int(act), float(eps), float(scale), xs, gs)
 
 
 def gated_norm_bwd_workspace_bytes(shape):
+    """Bytes for a GatedNormShape or a reference to one."""
     n = ctypes.c_size_t(0)
-    _check(load().sf_gdn_gated_norm_bwd_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+    _check(load().sf_gdn_gated_norm_bwd_workspace_size(shape, ctypes.byref(n)),
            "gated_norm_bwd_workspace_size")
     return n.value
 
@@ -613,8 +641,8 @@ def gated_norm_fwd(x, gate=None, w=None, eps=1e-6, scale=1.0, act=1, y=None, str
         y = torch.empty(full, dtype=x.dtype, device=dev)
         used_on(stream, y)
     _need(y, "y", x.dtype, full, dev)
-    _run("sf_gdn_gated_norm_fwd", dev, stream, ctypes.byref(shape), _ptr(x), _ptr(gate), _ptr(w),
-         _ptr(y))
+    _run("sf_gdn_gated_norm_fwd", dev, stream, shape, x.data_ptr(), _addr(gate), _addr(w),
+         y.data_ptr())
     return y
 
 
@@ -651,22 +679,23 @@ def gated_norm_bwd(x, gate, w, dy, eps=1e-6, scale=1.0, act=1, grads=None, want_
             used_on(stream, workspace)
     else:
         dw = workspace = None
-    wsn = ctypes.c_size_t(0 if workspace is None else workspace.numel())
-    _run("sf_gdn_gated_norm_bwd", dev, stream, ctypes.byref(shape), _ptr(x), _ptr(gate), _ptr(w),
-         _ptr(dy), _ptr(dx), _ptr(dgate), _ptr(dw), _ptr(workspace), wsn)
+    _run("sf_gdn_gated_norm_bwd", dev, stream, shape, x.data_ptr(), _addr(gate), _addr(w),
+         dy.data_ptr(), dx.data_ptr(), _addr(dgate), _addr(dw), _addr(workspace),
+         0 if workspace is None else workspace.numel())
     return dx, dgate, dw
 
 
 def residual_norm_shape(x, eps=1e-6, scale=1.0):
-    """ResidualNormShape of x [..., C]."""
+    """ResidualNormShape of x [..., C], by reference."""
     C = x.shape[-1]
-    return ResidualNormShape(x.numel() // C if C else 0, C, _dtype_code(x, "x"), float(eps),
-                             float(scale))
+    return _shape_ref(ResidualNormShape, x.numel() // C if C else 0, C, _dtype_code(x, "x"),
+                      float(eps), float(scale))
 
 
 def residual_norm_bwd_workspace_bytes(shape):
+    """Bytes for a ResidualNormShape or a reference to one."""
     n = ctypes.c_size_t(0)
-    _check(load().sf_gdn_residual_norm_bwd_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
+    _check(load().sf_gdn_residual_norm_bwd_workspace_size(shape, ctypes.byref(n)),
            "residual_norm_bwd_workspace_size")
     return n.value
 
@@ -680,9 +709,11 @@ def residual_norm_fwd(x, r=None, w=None, s=None, scale=1.0, eps=1e-6, h=None, y=
     dev = _device_of(x, "x")
     shape = residual_norm_shape(x, eps, scale)
     _need(x, "x", x.dtype, x.shape, dev)
-    for t, n in ((w, "w"), (s, "s")):
-        if t is not None:
-            _need(t, n, torch.float32, (shape.C,), dev)
+    vec = x.shape[-1:]
+    if w is not None:
+        _need(w, "w", torch.float32, vec, dev)
+    if s is not None:
+        _need(s, "s", torch.float32, vec, dev)
     if r is not None:
         _need(r, "r", x.dtype, x.shape, dev)
         if h is None:
@@ -695,8 +726,8 @@ def residual_norm_fwd(x, r=None, w=None, s=None, scale=1.0, eps=1e-6, h=None, y=
         y = torch.empty_like(x)
         used_on(stream, y)
     _need(y, "y", x.dtype, x.shape, dev)
-    _run("sf_gdn_residual_norm_fwd", dev, stream, ctypes.byref(shape), _ptr(x), _ptr(r), _ptr(s),
-         _ptr(w), _ptr(h), _ptr(y))
+    _run("sf_gdn_residual_norm_fwd", dev, stream, shape, x.data_ptr(), _addr(r), _addr(s),
+         _addr(w), _addr(h), y.data_ptr())
     return y, (x if r is None else h)
 
 
@@ -709,7 +740,7 @@ def residual_norm_bwd(h, r, w, s, dy, dh=None, scale=1.0, eps=1e-6, grads=None, 
     outputs in that order."""
     dev = _device_of(h, "h")
     shape = residual_norm_shape(h, eps, scale)
-    C = shape.C
+    C = h.shape[-1]
     _need(h, "h", h.dtype, h.shape, dev)
     _need(dy, "dy", h.dtype, h.shape, dev)
     if dh is not None:
@@ -741,11 +772,11 @@ def residual_norm_bwd(h, r, w, s, dy, dh=None, scale=1.0, eps=1e-6, grads=None, 
             used_on(stream, workspace)
     else:
         workspace = None
-    wsn = ctypes.c_size_t(0 if workspace is None else workspace.numel())
-    _run("sf_gdn_residual_norm_bwd", dev, stream, ctypes.byref(shape), _ptr(h),
-         _ptr(r) if want_ds else None, _ptr(s), _ptr(w), _ptr(dy), _ptr(dh), _ptr(dx),
-         _ptr(dr) if want_dr else None, _ptr(dw) if want_dw else None,
-         _ptr(ds) if want_ds else None, _ptr(workspace), wsn)
+    _run("sf_gdn_residual_norm_bwd", dev, stream, shape, h.data_ptr(),
+         r.data_ptr() if want_ds else None, _addr(s), _addr(w), dy.data_ptr(), _addr(dh),
+         dx.data_ptr(), dr.data_ptr() if want_dr else None, dw.data_ptr() if want_dw else None,
+         ds.data_ptr() if want_ds else None, _addr(workspace),
+         0 if workspace is None else workspace.numel())
     return dx, (dr if want_dr else None), (dw if want_dw else None), (ds if want_ds else None)
 
 

@@ -302,58 +302,101 @@ __global__ __launch_bounds__(CONV_THREADS) void conv_dw_reduce_kernel(const floa
 // ------------------------------------------------- single tokens over a pool
 // Serving: every sequence of a batch brings its new tokens and finds its last
 // W-1 inputs in its slot of a state pool, updated in place.  Thread: V
-// channels, with their taps in registers over the sequences that its
-// workgroup column walks.
+// channels of one sequence, which it walks in runs of CONV_STEP_RUN tokens
+// whose loads are issued together, a run ahead (the first one's beside the
+// state's), so that a decoding step waits for memory twice: for the batch's entry, and for
+// all of its inputs.
 constexpr int CONV_STEP_THREADS = 64;
+constexpr int CONV_STEP_RUN = 4;
+
+// Channel values as whole words: selects and loop-carried copies of them cost
+// a register per word.
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+template <typename T, int V> __device__ __forceinline__ void unpack(u32x4 r, float (&f)[V]);
+template <> __device__ __forceinline__ void unpack<bf16, 8>(u32x4 r, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(r[i] << 16);
+    f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
+  }
+}
+template <> __device__ __forceinline__ void unpack<float, 4>(u32x4 r, float (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r[i]);
+}
 
 template <typename T, int W, int V>
-__global__ __launch_bounds__(CONV_STEP_THREADS) void conv_step_kernel(ConvStepArgs a) {
-  const int c = (blockIdx.x * CONV_STEP_THREADS + threadIdx.x) * V;
-  const bool live = c < a.C;
+__global__ __launch_bounds__(CONV_STEP_THREADS) void conv_step_kernel(ConvStepArgs a, int groups) {
+  static_assert(sizeof(T) * V == 16, "16 bytes of channels per thread");
+  constexpr int R = CONV_STEP_RUN;
+  const int seq = blockIdx.x / groups;
+  const int c0 = ((blockIdx.x - seq * groups) * CONV_STEP_THREADS + threadIdx.x) * V;
+  const bool live = c0 < a.C;
+  const int c = live ? c0 : 0;  // lanes past the channels load channel 0's and store nothing
+  const SeqEntry e = seq_entry(a.b, seq);
   float wt[W][V];
 #pragma unroll
-  for (int j = 0; j < W; ++j)
+  for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int i = 0; i < V; ++i) wt[j][i] = live ? a.w[(size_t)(c + i) * W + j] : 0.f;
-  for (int seq = blockIdx.y; seq < a.b.n_seq; seq += gridDim.y) {
-    const SeqEntry e = seq_entry(a.b, seq);
-    if (e.slot < 0 || e.t0 >= e.t1) continue;
-    const bool bad = e.bad || (a.update && a.b.slots && slot_repeats(a.b, seq, e.slot));
-    if (!live) continue;
-    T* __restrict__ y = reinterpret_cast<T*>(a.y) + c;
-    if (bad) {
-      float nan[V];
+    for (int j = 0; j < W; ++j) wt[j][i] = a.w[(size_t)(c + i) * W + j];
+  if (e.slot < 0 || e.t0 >= e.t1) return;
+  T* __restrict__ y = reinterpret_cast<T*>(a.y) + c;
+  const T* __restrict__ x = reinterpret_cast<const T*>(a.x) + c;
+  T* state = reinterpret_cast<T*>(a.state);
+  u32x4 in[W - 1 + R];  // the W-1 inputs before a run, then the run
+  u32x4 nx[R];          // the next run
+  auto load = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) nan[i] = __builtin_nanf("");
-      for (int t = e.t0; t < e.t1; ++t) st_vec<T, V>(y + (size_t)t * a.C, nan);
-      continue;
-    }
-    const T* __restrict__ x = reinterpret_cast<const T*>(a.x) + c;
-    T* state = reinterpret_cast<T*>(a.state) + (size_t)e.slot * (W - 1) * a.C + c;
-    float win[W][V];  // win[j] = the input j tokens before the current one
+    for (int r = 0; r < R; ++r)
+      if (t + r < e.t1) nx[r] = *reinterpret_cast<const u32x4*>(x + (size_t)(t + r) * a.xs);
+  };
+  if (!e.bad) {
+    state += (size_t)e.slot * (W - 1) * a.C + c;
 #pragma unroll
-    for (int j = 1; j < W; ++j) ld_vec<T, V>(state + (size_t)(W - 1 - j) * a.C, win[j]);
-#pragma unroll 4
-    for (int t = e.t0; t < e.t1; ++t) {
-      ld_vec<T, V>(x + (size_t)t * a.xs, win[0]);
-      float z[V];
+    for (int j = 0; j < W - 1; ++j) in[j] = *reinterpret_cast<const u32x4*>(state + (size_t)j * a.C);
+    load(e.t0);
+  }
+  if (e.bad || (a.update && a.b.slots && slot_repeats(a.b, seq, e.slot))) {
+    float nan[V];
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float s = 0.f;
+    for (int i = 0; i < V; ++i) nan[i] = __builtin_nanf("");
+    for (int t = e.t0; t < e.t1 && live; ++t) st_vec<T, V>(y + (size_t)t * a.C, nan);
+    return;
+  }
+  for (int t = e.t0; t < e.t1; t += R) {
+    const int n = min(R, e.t1 - t);
 #pragma unroll
-        for (int j = 0; j < W; ++j) s += wt[j][i] * win[j][i];
-        z[i] = a.act ? silu(s) : s;
+    for (int r = 0; r < R; ++r) in[W - 1 + r] = nx[r];
+    load(t + R);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (r >= n) break;
+      float z[V] = {};
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        float f[V];
+        unpack<T, V>(in[W - 1 + r - j], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] += wt[j][i] * f[i];
       }
-      st_vec<T, V>(y + (size_t)t * a.C, z);
+      if (a.act) {
 #pragma unroll
-      for (int j = W - 1; j >= 1; --j)
-#pragma unroll
-        for (int i = 0; i < V; ++i) win[j][i] = win[j - 1][i];
+        for (int i = 0; i < V; ++i) z[i] = silu(z[i]);
+      }
+      if (live) st_vec<T, V>(y + (size_t)(t + r) * a.C, z);
     }
-    if (a.update) {
+    // the last W-1 inputs up to token t + n - 1
 #pragma unroll
-      for (int j = 1; j < W; ++j) st_vec<T, V>(state + (size_t)(W - 1 - j) * a.C, win[j]);
+    for (int j = 0; j < W - 1; ++j) {
+      u32x4 p = in[j + 1];
+#pragma unroll
+      for (int m = 2; m <= R; ++m) p = n == m ? in[j + m] : p;
+      in[j] = p;
     }
+  }
+  if (a.update && live) {
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<u32x4*>(state + (size_t)j * a.C) = in[j];
   }
 }
 
@@ -448,8 +491,8 @@ static hipError_t conv_step_w(const ConvStepArgs& a, hipStream_t st, Profiler* p
   constexpr int V = conv_vf<T>();
   const int gx = (a.C / V + CONV_STEP_THREADS - 1) / CONV_STEP_THREADS;
   prof_begin(prof, "conv_step", st);
-  hipLaunchKernelGGL((conv_step_kernel<T, W, V>), dim3(gx, a.b.n_seq < 65535 ? a.b.n_seq : 65535),
-                     dim3(CONV_STEP_THREADS), 0, st, a);
+  hipLaunchKernelGGL((conv_step_kernel<T, W, V>), dim3((unsigned)gx * a.b.n_seq),
+                     dim3(CONV_STEP_THREADS), 0, st, a, gx);
   prof_end(prof, st);
   return hipGetLastError();
 }

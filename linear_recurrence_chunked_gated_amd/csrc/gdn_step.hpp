@@ -47,139 +47,252 @@ __device__ __forceinline__ bool slot_repeats(const PoolBatch& b, int i, int slot
   return __any(hit);
 }
 
-// sum over the 8 lanes of a half row; every lane ends with the total
-__device__ __forceinline__ float sum_half_row8(float x) {
+// Sums over a row's D columns come out the same, bit for bit, on 8 and on 16
+// lanes and for a token that came alone or among others, so that a sequence's
+// outputs do not depend on how it was batched: columns go in units of four,
+// unit c of a row is summed with unit c + 16 (where D has it), that with unit
+// c + 8's sum, and the eight results in a tree.
+//
+// x: this lane's part, on 16 lanes the sum of units l and l + 16, on 8 lanes
+// already joined with units l + 8 and l + 24; every lane gets the total.
+template <int L>
+__device__ __forceinline__ float sum_row_lanes(float x) {
+  if (L == 16) x += dpp_f<0x128>(x);  // rotate by 8 within the 16 lanes
   x += dpp_f<0xB1>(x);
   x += dpp_f<0x4E>(x);
   x += dpp_f<0x141>(x);
   return x;
 }
+__device__ __forceinline__ float add4(f32x4 x) { return (x[0] + x[1]) + (x[2] + x[3]); }
+// S . k over the row, in every lane
+template <int NE, int L>
+__device__ __forceinline__ float row_dot(const f32x4 (&S)[NE], const f32x4 (&k)[NE]) {
+  constexpr int H = L == 8 ? 2 : 1;  // separate sums in a lane
+  f32x4 s[H];
+#pragma unroll
+  for (int j = 0; j < NE; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      s[j % H][i] = j < H ? S[j][i] * k[j][i] : __builtin_fmaf(S[j][i], k[j][i], s[j % H][i]);
+  float x = add4(s[0]);
+  if (H == 2) x += add4(s[1]);
+  return sum_row_lanes<L>(x);
+}
+// one unit of k . q
+__device__ __forceinline__ float unit_dot(f32x4 k, f32x4 q) {
+  return __builtin_fmaf(k[3], q[3],
+                        __builtin_fmaf(k[2], q[2], __builtin_fmaf(k[1], q[1], k[0] * q[0])));
+}
 
 constexpr int STEP_THREADS = 256;
+// Tokens staged in LDS at a time: two buffers stay under 20 KB, so that eight
+// workgroups share a compute unit.
+constexpr int STEP_TOKENS = 8;
 
-template <typename T> struct Row4 {
-  typedef T vec __attribute__((ext_vector_type(4)));
-};
-
-// Workgroup: 4 waves, wave w rows r0 + 8 NR w .. of one (sequence, value
-// head); NR row groups of 8 rows per wave.
-template <typename T, int D, int NR>
+// Workgroup: 4 waves, each of 64 / L rows of one (sequence, value head)'s
+// state, a row on L lanes.  SINGLE: one token per sequence, straight from
+// global memory with the state.  Otherwise the tokens are staged through LDS
+// a chunk ahead, as floats and with k . q beside them, since a token's
+// arithmetic is far shorter than a load and each wave would repeat both.
+// STREAM: the states bypass the caches (see launch_recurrent_step).
+template <typename T, int D, int L, bool SINGLE, bool STREAM>
 __global__ __launch_bounds__(STEP_THREADS) void recurrent_step_kernel(StepArgs a) {
-  typedef typename Row4<T>::vec vec4;
-  constexpr int NE = D / 32;  // 4-column pieces per lane
-  constexpr int PARTS = D / (32 * NR);
+  constexpr int NE = D / (4 * L);        // 4-column pieces per lane
+  constexpr int WROWS = 64 / L;          // rows of a wave
+  constexpr int ROWS = 4 * WROWS;        // rows of the workgroup
+  constexpr int PARTS = D / ROWS;
   const int part = blockIdx.x % PARTS;
   const int sh = blockIdx.x / PARTS;
   const int hv = sh % a.Hv, seq = sh / a.Hv;
   const SeqEntry e = seq_entry(a.b, seq);
   if (e.slot < 0 || e.t0 >= e.t1) return;
-  const int lane = lane_id(), l8 = lane & 7;
-  const int r0 = (part * 4 + wave_id()) * 8 * NR;  // first row of this wave
-  const int row = r0 + (lane >> 3);                // row group r: row + 8 r
-  T* __restrict__ o = reinterpret_cast<T*>(a.o) + (size_t)hv * D + r0;
+  const int lane = lane_id(), l = lane % L;
+  const int wrow = wave_id() * WROWS + lane / L;  // this lane's row in the workgroup
+  const int r0 = part * ROWS;
+  T* __restrict__ o = reinterpret_cast<T*>(a.o) + (size_t)hv * D + r0 + wrow;
   const size_t os = (size_t)a.Hv * D;
-  // lane (group g = lane / 8, l8) writes output row 8 l8 + g, for l8 < NR
-  const int orow = 8 * l8 + (lane >> 3);
 
-  float4 S[NR][NE];
+  f32x4 S[NE];
   float* Sp = a.state;
   if (!e.bad) {
-    Sp += ((size_t)e.slot * a.Hv + hv) * D * D + (size_t)row * D + l8 * 4;
+    Sp += ((size_t)e.slot * a.Hv + hv) * D * D + (size_t)(r0 + wrow) * D + l * 4;
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-      for (int j = 0; j < NE; ++j) S[r][j] = *reinterpret_cast<const float4*>(Sp + r * 8 * D + j * 32);
+    for (int j = 0; j < NE; ++j) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(Sp + j * 4 * L);
+      S[j] = STREAM ? __builtin_nontemporal_load(p) : *p;
+    }
   }
   const bool bad = e.bad || (a.update && a.b.slots && slot_repeats(a.b, seq, e.slot));
   if (bad) {
-    if (l8 < NR)
-      for (int t = e.t0; t < e.t1; ++t) o[t * os + orow] = (T)__builtin_nanf("");
+    if (l == 0)
+      for (int t = e.t0; t < e.t1; ++t) o[t * os] = (T)__builtin_nanf("");
     return;
   }
   const int hk = hv / a.group;
-  const T* __restrict__ q = reinterpret_cast<const T*>(a.q) + (size_t)hk * D + l8 * 4;
-  const T* __restrict__ k = reinterpret_cast<const T*>(a.k) + (size_t)hk * D + l8 * 4;
-  const T* __restrict__ v = reinterpret_cast<const T*>(a.v) + (size_t)hv * D + row;
+  const T* __restrict__ q = reinterpret_cast<const T*>(a.q) + (size_t)hk * D;
+  const T* __restrict__ k = reinterpret_cast<const T*>(a.k) + (size_t)hk * D;
+  const T* __restrict__ v = reinterpret_cast<const T*>(a.v) + (size_t)hv * D + r0;
 
-  vec4 kn[NE], qn[NE];
-  T vn[NR];
-  float an, bn;
-  auto fetch = [&](int t) {
+  struct Token {
+    f32x4 k[NE], q[NE];
+    f32x4 g;  // alpha, beta, k . q
+    float v;
+  };
+  auto token = [&](T* ot, const Token& x) {
+    const float p = row_dot<NE, L>(S, x.k), s = row_dot<NE, L>(S, x.q);
+    const float u = x.g[1] * __builtin_fmaf(-x.g[0], p, x.v);
+    const float y = __builtin_fmaf(u, x.g[2], x.g[0] * s);
+    if (l == 0) *ot = (T)y;
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[j][i] = __builtin_fmaf(u, x.k[j][i], x.g[0] * S[j][i]);
+  };
+
+  if constexpr (SINGLE) {
+    typedef T vec4 __attribute__((ext_vector_type(4)));
+    const size_t t = e.t0;
+    Token x;
+    float kq[NE];
 #pragma unroll
     for (int j = 0; j < NE; ++j) {
-      kn[j] = *reinterpret_cast<const vec4*>(k + (size_t)t * a.ks + j * 32);
-      qn[j] = *reinterpret_cast<const vec4*>(q + (size_t)t * a.qs + j * 32);
+      x.k[j] = __builtin_convertvector(
+          *reinterpret_cast<const vec4*>(k + t * a.ks + (j * L + l) * 4), f32x4);
+      x.q[j] = __builtin_convertvector(
+          *reinterpret_cast<const vec4*>(q + t * a.qs + (j * L + l) * 4), f32x4);
+      kq[j] = unit_dot(x.k[j], x.q[j]);
     }
+    constexpr int U = 16 / L;  // units l (and l + 8) of this lane, each with the one 16 on
 #pragma unroll
-    for (int r = 0; r < NR; ++r) vn[r] = v[(size_t)t * a.vs + r * 8];
-    an = a.alpha[(size_t)t * a.Hv + hv];
-    bn = a.beta[(size_t)t * a.Hv + hv];
-  };
-  fetch(e.t0);
-  for (int t = e.t0; t < e.t1; ++t) {
-    float kf[NE][4], qf[NE][4], vf[NR];
+    for (int j = U; j < NE; ++j) kq[j - U] += kq[j];
+    if (U == 2) kq[0] += kq[1];
+    x.v = (float)v[t * a.vs + wrow];
+    x.g[0] = a.alpha[t * a.Hv + hv];
+    x.g[1] = a.beta[t * a.Hv + hv];
+    x.g[2] = sum_row_lanes<L>(kq[0]);
+    token(o + t * os, x);
+  } else {
+    // Staging: 32 threads per token, each with a unit of four columns of k
+    // and q (half of the threads at D = 64) and the token's rows of v spread
+    // over them.
+    constexpr int TB = STEP_TOKENS;
+    constexpr int VV = (ROWS + 31) / 32;
+    static_assert(TB * 32 == STEP_THREADS, "one token per 32 threads");
+    typedef T vec4 __attribute__((ext_vector_type(4)));
+    struct Chunk {
+      f32x4 k[TB][D / 4], q[TB][D / 4];
+      float v[TB][VV * 32];
+      f32x4 g[TB];  // alpha, beta, k . q
+    };
+    __shared__ Chunk lds[2];
+    const int st = threadIdx.x / 32, sl = threadIdx.x % 32;  // token of the chunk, thread in it
+    const int su = sl % (D / 4);                             // its unit
+    vec4 rk, rq;
+    T rv[VV];
+    float ra = 0.f, rb = 0.f;
+    auto load = [&](int c) {
+      const size_t t = min(c + st, e.t1 - 1);  // past the end: the last token again, not used
+      rk = *reinterpret_cast<const vec4*>(k + t * a.ks + su * 4);
+      rq = *reinterpret_cast<const vec4*>(q + t * a.qs + su * 4);
 #pragma unroll
-    for (int j = 0; j < NE; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        kf[j][i] = (float)kn[j][i];
-        qf[j][i] = (float)qn[j][i];
+      for (int i = 0; i < VV; ++i) rv[i] = v[t * a.vs + min(i * 32 + sl, ROWS - 1)];
+      ra = a.alpha[t * a.Hv + hv];
+      rb = a.beta[t * a.Hv + hv];
+    };
+    auto store = [&](Chunk& b) {
+      const f32x4 kf = __builtin_convertvector(rk, f32x4), qf = __builtin_convertvector(rq, f32x4);
+      float kq = unit_dot(kf, qf);
+      if (D == 128) kq += __shfl_xor(kq, 16);
+      kq = sum_row_lanes<16>(kq);
+      if (sl < D / 4) {
+        b.k[st][su] = kf;
+        b.q[st][su] = qf;
       }
 #pragma unroll
-    for (int r = 0; r < NR; ++r) vf[r] = (float)vn[r];
-    const float al = an, be = bn;
-    if (t + 1 < e.t1) fetch(t + 1);
-    float kq = 0.f;
+      for (int i = 0; i < VV; ++i) b.v[st][i * 32 + sl] = (float)rv[i];
+      if (sl == 0) b.g[st] = f32x4{ra, rb, kq, 0.f};
+    };
+    load(e.t0);
+    T* ot = o + e.t0 * os;
+#pragma unroll 1
+    for (int c = e.t0, buf = 0; c < e.t1; c += TB, buf ^= 1) {
+      // this buffer's readers (two chunks back) have passed the last barrier
+      store(lds[buf]);
+      __syncthreads();
+      if (c + TB < e.t1) load(c + TB);
+      const Chunk& b = lds[buf];
+      const int m = min(TB, e.t1 - c);
+      auto read = [&](int i, Token& x) {
 #pragma unroll
-    for (int j = 0; j < NE; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) kq += kf[j][i] * qf[j][i];
-    kq = sum_half_row8(kq);
-    float out = 0.f;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      float p = 0.f, s = 0.f;
-#pragma unroll
-      for (int j = 0; j < NE; ++j) {
-        const float4 x = S[r][j];
-        p += x.x * kf[j][0] + x.y * kf[j][1] + x.z * kf[j][2] + x.w * kf[j][3];
-        s += x.x * qf[j][0] + x.y * qf[j][1] + x.z * qf[j][2] + x.w * qf[j][3];
-      }
-      p = sum_half_row8(p);
-      s = sum_half_row8(s);
-      const float u = be * (vf[r] - al * p);
-      const float y = al * s + u * kq;
-      out = l8 == r ? y : out;
-#pragma unroll
-      for (int j = 0; j < NE; ++j) {
-        S[r][j].x = al * S[r][j].x + u * kf[j][0];
-        S[r][j].y = al * S[r][j].y + u * kf[j][1];
-        S[r][j].z = al * S[r][j].z + u * kf[j][2];
-        S[r][j].w = al * S[r][j].w + u * kf[j][3];
+        for (int j = 0; j < NE; ++j) {
+          x.k[j] = b.k[i][j * L + l];
+          x.q[j] = b.q[i][j * L + l];
+        }
+        x.g = b.g[i];
+        x.v = b.v[i][wrow];
+      };
+      Token x;
+      if (L == 16) {
+        // few workgroups, few waves to hide the LDS reads: a token ahead
+        read(0, x);
+#pragma unroll 1
+        for (int i = 0; i < m; ++i, ot += os) {
+          Token y;
+          read(min(i + 1, m - 1), y);
+          token(ot, x);
+          x = y;
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < m; ++i, ot += os) {
+          read(i, x);
+          token(ot, x);
+        }
       }
     }
-    if (l8 < NR) o[t * os + orow] = (T)out;
   }
   if (a.update) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
-#pragma unroll
-      for (int j = 0; j < NE; ++j) *reinterpret_cast<float4*>(Sp + r * 8 * D + j * 32) = S[r][j];
+    for (int j = 0; j < NE; ++j) {
+      f32x4* p = reinterpret_cast<f32x4*>(Sp + j * 4 * L);
+      if (STREAM)
+        __builtin_nontemporal_store(S[j], p);
+      else
+        *p = S[j];
+    }
   }
 }
 
-template <typename T, int D, int NR>
-static hipError_t step_nr(const StepArgs& a, hipStream_t st, Profiler* prof) {
-  const unsigned grid = (unsigned)((size_t)a.b.n_seq * a.Hv * (D / (32 * NR)));
+template <typename T, int D, int L, bool SINGLE, bool STREAM>
+static hipError_t step_launch(const StepArgs& a, hipStream_t st, Profiler* prof) {
+  const unsigned grid = (unsigned)((size_t)a.b.n_seq * a.Hv * (D * L / 256));
   prof_begin(prof, "recurrent_step", st);
-  hipLaunchKernelGGL((recurrent_step_kernel<T, D, NR>), dim3(grid), dim3(STEP_THREADS), 0, st, a);
+  hipLaunchKernelGGL((recurrent_step_kernel<T, D, L, SINGLE, STREAM>), dim3(grid),
+                     dim3(STEP_THREADS), 0, st, a);
   prof_end(prof, st);
   return hipGetLastError();
 }
 
+// The variants, each against the other on an MI355X (bf16, D = 128, 16 heads):
+//  - states of 128 MiB or more in one call cannot stay in the 256 MB last-level
+//    cache until the next one: non-temporal loads and stores take 183 us
+//    instead of 203 for 512 MiB and 50 instead of 53 for 128 MiB, but 37.3
+//    instead of 36.2 for 96 MiB and 19.9 instead of 17.3 for 48 MiB;
+//  - with several tokens and too few workgroups of eight-lane rows to give
+//    every compute unit one, 16 lanes a row halve each token's arithmetic:
+//    one sequence of 256 tokens 65 us instead of 83, two of 8 tokens 4.5
+//    instead of 5.1; at 256 workgroups both take 5.4 and beyond, the eight
+//    lanes are faster (8 sequences of 8 tokens 7.5 instead of 8.6).
 template <typename T, int D>
 hipError_t launch_recurrent_step(const StepArgs& a, hipStream_t st, Profiler* prof) {
-  return step_nr<T, D, 1>(a, st, prof);
+  const size_t heads = (size_t)a.b.n_seq * a.Hv;
+  const bool stream = heads * D * D * sizeof(float) >= (size_t)128 << 20;
+  if (!a.b.seq_start && a.b.uniform == 1)
+    return stream ? step_launch<T, D, 8, true, true>(a, st, prof)
+                  : step_launch<T, D, 8, true, false>(a, st, prof);
+  if (stream) return step_launch<T, D, 8, false, true>(a, st, prof);
+  if (heads * (D / 32) < 256) return step_launch<T, D, 16, false, false>(a, st, prof);
+  return step_launch<T, D, 8, false, false>(a, st, prof);
 }
 
 template hipError_t launch_recurrent_step<bf16, 64>(const StepArgs&, hipStream_t, Profiler*);

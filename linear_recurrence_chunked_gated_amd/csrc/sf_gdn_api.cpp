@@ -920,6 +920,8 @@ sf_status sf_gdn_shortconv_step(const sf_conv_step_shape* shape, const void* x, 
   if (p.act != 0 && p.act != 1) return fail(SF_ERR_INVALID_ARG, "act must be 0 or 1");
   if (p.update != 0 && p.update != 1) return fail(SF_ERR_INVALID_ARG, "update must be 0 or 1");
   if (p.C % 8 || p.C > (1 << 24)) return fail(SF_ERR_UNSUPPORTED, "C must be a multiple of 8, at most 2^24");
+  // a launch holds 2^32 threads, one for at least 4 channels of a sequence
+  if ((long long)p.n_seq * (p.C + 512) > (1LL << 32)) return fail(SF_ERR_UNSUPPORTED, "n_seq * C too large");
   if ((s = make_batch(p.n_seq, p.n_tok, p.n_slots, slots, seq_start, a.b)) != SF_OK) return s;
   if ((s = token_stride(p.x_stride, p.C, "x", &a.xs)) != SF_OK) return s;
   if (p.n_seq == 0 || p.n_tok == 0) return SF_OK;
