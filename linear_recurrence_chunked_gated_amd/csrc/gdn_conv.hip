@@ -304,8 +304,8 @@ __global__ __launch_bounds__(CONV_THREADS) void conv_dw_reduce_kernel(const floa
 // W-1 inputs in its slot of a state pool, updated in place.  Thread: V
 // channels of one sequence, which it walks in runs of CONV_STEP_RUN tokens
 // whose loads are issued together, a run ahead (the first one's beside the
-// state's), so that a decoding step waits for memory twice: for the batch's entry, and for
-// all of its inputs.
+// state's), so that a decoding step waits for memory twice: for the batch's
+// entry, and for all of its inputs.
 constexpr int CONV_STEP_THREADS = 64;
 constexpr int CONV_STEP_RUN = 4;
 

@@ -962,8 +962,8 @@ sf_status make_gated(const sf_gated_norm_shape* p, GatedNormArgs& a) {
     return fail(SF_ERR_UNSUPPORTED, "D must be a multiple of 8, at most 512");
   if (p->act != 0 && p->act != 1) return fail(SF_ERR_INVALID_ARG, "act must be 0 or 1");
   if (!(p->eps >= 0.f)) return fail(SF_ERR_INVALID_ARG, "eps must be >= 0");
-  if (p->N > (1LL << 40) / p->H || p->N * p->H > (1LL << 40) / p->D)
-    return fail(SF_ERR_UNSUPPORTED, "too large");
+  // the kernels count head rows in 32 bits, and step past the last ones
+  if (p->N > (1LL << 31) / p->H) return fail(SF_ERR_UNSUPPORTED, "N * H too large");
   const long long row = (long long)p->H * p->D;
   if ((s = token_stride(p->x_stride, row, "x", &a.xs)) != SF_OK) return s;
   if ((s = token_stride(p->gate_stride, row, "gate", &a.gs)) != SF_OK) return s;
