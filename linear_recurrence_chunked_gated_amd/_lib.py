@@ -452,9 +452,17 @@ def shortconv_bwd(x, w, conv_in, dy, dconv_out=None, act=0, dx=None, dw=None, wa
 
 
 def _device_of(t, name):
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError("tensors must be on a GPU device (%s is on %s)" % (name, t.device))
     return t.device
+
+
+def _empty(like, shape):
+    """A contiguous tensor of `shape`, in the type and on the device of `like`
+    (empty_like is the cheaper call)."""
+    if like.shape == shape and like.is_contiguous():
+        return torch.empty_like(like)
+    return torch.empty(shape, dtype=like.dtype, device=like.device)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -478,7 +486,7 @@ def _run(fn, dev, stream, *args):
     else:
         raw = stream.cuda_stream
     call = getattr(_lib or load(), fn)
-    if torch.cuda.current_device() == dev.index:
+    if torch._C._cuda_getDevice() == dev.index:
         st = call(*args, raw)
     else:
         with torch.cuda.device(dev):
@@ -558,9 +566,10 @@ def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=No
     _need(state, "state", torch.float32, (state.shape[0], Hv, Dv, Dk), dev)
     n_seq = _batch(slots, seq_start, state.shape[0], dev)
     if o is None:
-        o = torch.empty((N, Hv, Dv), dtype=q.dtype, device=dev)
+        o = _empty(v, (N, Hv, Dv))
         used_on(stream, o)
-    _need(o, "o", q.dtype, (N, Hv, Dv), dev)
+    else:
+        _need(o, "o", q.dtype, (N, Hv, Dv), dev)
     shape = _shape_ref(StepShape, n_seq, N, state.shape[0], Hk, Hv, Dk, Dv, code,
                        1 if update else 0, qs, ks, vs)
     _run("sf_gdn_recurrent_step", dev, stream, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(),
@@ -588,9 +597,10 @@ def shortconv_step(x, w, state, slots=None, seq_start=None, act=0, y=None, updat
     _need(state, "state", x.dtype, (state.shape[0], W - 1, C), dev)
     n_seq = _batch(slots, seq_start, state.shape[0], dev)
     if y is None:
-        y = torch.empty((N, C), dtype=x.dtype, device=dev)
+        y = _empty(x, (N, C))
         used_on(stream, y)
-    _need(y, "y", x.dtype, (N, C), dev)
+    else:
+        _need(y, "y", x.dtype, (N, C), dev)
     shape = _shape_ref(ConvStepShape, n_seq, N, state.shape[0], C, W, code, int(act),
                        1 if update else 0, xs)
     _run("sf_gdn_shortconv_step", dev, stream, shape, x.data_ptr(), w.data_ptr(), _addr(slots),
@@ -605,23 +615,39 @@ def _heads(x):
     return x if x.dim() == 3 else x.view(-1, x.shape[-2], x.shape[-1])
 
 
-def gated_norm_shape(x, gate=None, eps=1e-6, scale=1.0, act=1):
-    """GatedNormShape of x [N, H, D] and gate, which are checked, by
-    reference."""
+def _gated_norm_fields(x, gate, eps, scale, act):
+    """GatedNormShape's fields for x [N, H, D] and gate, which are checked."""
     dev = _device_of(x, "x")
     code = _dtype_code(x, "x")
     full = N, H, D = x.shape
     xs = _token_rows(x, "x", x.dtype, full, dev)
     gs = 0 if gate is None else _token_rows(gate, "gate", x.dtype, full, dev)
-    return _shape_ref(GatedNormShape, N, H, D, code, int(act), float(eps), float(scale), xs, gs)
+    return N, H, D, code, int(act), float(eps), float(scale), xs, gs
 
 
 def gated_norm_bwd_workspace_bytes(shape):
-    """Bytes for a GatedNormShape or a reference to one."""
     n = ctypes.c_size_t(0)
-    _check(load().sf_gdn_gated_norm_bwd_workspace_size(shape, ctypes.byref(n)),
+    _check(load().sf_gdn_gated_norm_bwd_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
            "gated_norm_bwd_workspace_size")
     return n.value
+
+
+def _norm_workspace(query, cls, fields, workspace, dev, stream):
+    """The caller's workspace if it is large enough, else a new one."""
+    need = _norm_bytes(query, cls, *fields)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
+    if need > 0 and (workspace is None or workspace.numel() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        if workspace.data_ptr() % 256:
+            workspace = alloc_workspace(need, dev)
+        used_on(stream, workspace)
+    return workspace
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_bytes(query, cls, *fields):
+    return query(cls(*fields))
 
 
 def gated_norm_fwd(x, gate=None, w=None, eps=1e-6, scale=1.0, act=1, y=None, stream=None):
@@ -633,14 +659,15 @@ def gated_norm_fwd(x, gate=None, w=None, eps=1e-6, scale=1.0, act=1, y=None, str
     full = x.shape
     x = _heads(x)
     gate = None if gate is None else _heads(gate)
-    shape = gated_norm_shape(x, gate, eps, scale, act)
+    shape = _shape_ref(GatedNormShape, *_gated_norm_fields(x, gate, eps, scale, act))
     dev = x.device
     if w is not None:
         _need(w, "w", torch.float32, (x.shape[2],), dev)
     if y is None:
-        y = torch.empty(full, dtype=x.dtype, device=dev)
+        y = _empty(x, full)
         used_on(stream, y)
-    _need(y, "y", x.dtype, full, dev)
+    else:
+        _need(y, "y", x.dtype, full, dev)
     _run("sf_gdn_gated_norm_fwd", dev, stream, shape, x.data_ptr(), _addr(gate), _addr(w),
          y.data_ptr())
     return y
@@ -654,7 +681,7 @@ def gated_norm_bwd(x, gate, w, dy, eps=1e-6, scale=1.0, act=1, grads=None, want_
     full = x.shape
     x = _heads(x)
     gate = None if gate is None else _heads(gate)
-    shape = gated_norm_shape(x, gate, eps, scale, act)
+    fields = _gated_norm_fields(x, gate, eps, scale, act)
     dev, D = x.device, x.shape[2]
     if w is not None:
         _need(w, "w", torch.float32, (D,), dev)
@@ -673,29 +700,25 @@ def gated_norm_bwd(x, gate, w, dy, eps=1e-6, scale=1.0, act=1, grads=None, want_
         raise ValueError("dgate without gate")
     if want_dw:
         _need(dw, "dw", torch.float32, (D,), dev)
-        need = gated_norm_bwd_workspace_bytes(shape)
-        if workspace is None or workspace.numel() < need:
-            workspace = alloc_workspace(need, dev)
-            used_on(stream, workspace)
+        workspace = _norm_workspace(gated_norm_bwd_workspace_bytes, GatedNormShape, fields,
+                                    workspace, dev, stream)
     else:
         dw = workspace = None
-    _run("sf_gdn_gated_norm_bwd", dev, stream, shape, x.data_ptr(), _addr(gate), _addr(w),
-         dy.data_ptr(), dx.data_ptr(), _addr(dgate), _addr(dw), _addr(workspace),
-         0 if workspace is None else workspace.numel())
+    _run("sf_gdn_gated_norm_bwd", dev, stream, _shape_ref(GatedNormShape, *fields), x.data_ptr(),
+         _addr(gate), _addr(w), dy.data_ptr(), dx.data_ptr(), _addr(dgate), _addr(dw),
+         _addr(workspace), 0 if workspace is None else workspace.numel())
     return dx, dgate, dw
 
 
-def residual_norm_shape(x, eps=1e-6, scale=1.0):
-    """ResidualNormShape of x [..., C], by reference."""
+def _residual_norm_fields(x, eps, scale):
+    """ResidualNormShape's fields for x [..., C]."""
     C = x.shape[-1]
-    return _shape_ref(ResidualNormShape, x.numel() // C if C else 0, C, _dtype_code(x, "x"),
-                      float(eps), float(scale))
+    return (x.numel() // C if C else 0), C, _dtype_code(x, "x"), float(eps), float(scale)
 
 
 def residual_norm_bwd_workspace_bytes(shape):
-    """Bytes for a ResidualNormShape or a reference to one."""
     n = ctypes.c_size_t(0)
-    _check(load().sf_gdn_residual_norm_bwd_workspace_size(shape, ctypes.byref(n)),
+    _check(load().sf_gdn_residual_norm_bwd_workspace_size(ctypes.byref(shape), ctypes.byref(n)),
            "residual_norm_bwd_workspace_size")
     return n.value
 
@@ -707,7 +730,7 @@ def residual_norm_fwd(x, r=None, w=None, s=None, scale=1.0, eps=1e-6, h=None, y=
     with r like x (None: h is x), s [C] fp32 (None: ones) and w [C] fp32
     (None: ones).  Returns (y, h)."""
     dev = _device_of(x, "x")
-    shape = residual_norm_shape(x, eps, scale)
+    shape = _shape_ref(ResidualNormShape, *_residual_norm_fields(x, eps, scale))
     _need(x, "x", x.dtype, x.shape, dev)
     vec = x.shape[-1:]
     if w is not None:
@@ -719,13 +742,15 @@ def residual_norm_fwd(x, r=None, w=None, s=None, scale=1.0, eps=1e-6, h=None, y=
         if h is None:
             h = torch.empty_like(x)
             used_on(stream, h)
-        _need(h, "h", x.dtype, x.shape, dev)
+        else:
+            _need(h, "h", x.dtype, x.shape, dev)
     elif s is not None or h is not None:
         raise ValueError("s and h need r")
     if y is None:
         y = torch.empty_like(x)
         used_on(stream, y)
-    _need(y, "y", x.dtype, x.shape, dev)
+    else:
+        _need(y, "y", x.dtype, x.shape, dev)
     _run("sf_gdn_residual_norm_fwd", dev, stream, shape, x.data_ptr(), _addr(r), _addr(s),
          _addr(w), _addr(h), y.data_ptr())
     return y, (x if r is None else h)
@@ -739,7 +764,7 @@ def residual_norm_bwd(h, r, w, s, dy, dh=None, scale=1.0, eps=1e-6, grads=None, 
     for ds only and may be None otherwise); ``grads`` may supply preallocated
     outputs in that order."""
     dev = _device_of(h, "h")
-    shape = residual_norm_shape(h, eps, scale)
+    fields = _residual_norm_fields(h, eps, scale)
     C = h.shape[-1]
     _need(h, "h", h.dtype, h.shape, dev)
     _need(dy, "dy", h.dtype, h.shape, dev)
@@ -764,17 +789,14 @@ def residual_norm_bwd(h, r, w, s, dy, dh=None, scale=1.0, eps=1e-6, grads=None, 
     for t, n, want in ((dw, "dw", want_dw), (ds, "ds", want_ds)):
         if want:
             _need(t, n, torch.float32, (C,), dev)
-    need = 0
     if want_dw or want_ds:
-        need = residual_norm_bwd_workspace_bytes(shape)
-        if workspace is None or workspace.numel() < need:
-            workspace = alloc_workspace(need, dev)
-            used_on(stream, workspace)
+        workspace = _norm_workspace(residual_norm_bwd_workspace_bytes, ResidualNormShape, fields,
+                                    workspace, dev, stream)
     else:
         workspace = None
-    _run("sf_gdn_residual_norm_bwd", dev, stream, shape, h.data_ptr(),
-         r.data_ptr() if want_ds else None, _addr(s), _addr(w), dy.data_ptr(), _addr(dh),
-         dx.data_ptr(), dr.data_ptr() if want_dr else None, dw.data_ptr() if want_dw else None,
+    _run("sf_gdn_residual_norm_bwd", dev, stream, _shape_ref(ResidualNormShape, *fields),
+         h.data_ptr(), r.data_ptr() if want_ds else None, _addr(s), _addr(w), dy.data_ptr(),
+         _addr(dh), dx.data_ptr(), dr.data_ptr() if want_dr else None, dw.data_ptr() if want_dw else None,
          ds.data_ptr() if want_ds else None, _addr(workspace),
          0 if workspace is None else workspace.numel())
     return dx, (dr if want_dr else None), (dw if want_dw else None), (ds if want_ds else None)
