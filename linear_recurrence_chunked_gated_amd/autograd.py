@@ -15,8 +15,10 @@ sequence.  short_conv is the causal depthwise convolution ahead of the
 recurrence (sf_gdn_shortconv_fwd / _bwd), whose W-1-token boundary state
 chains the same way.  gated_norm and residual_norm are the layer's norms after
 and before the recurrence (sf_gdn_gated_norm_*, sf_gdn_residual_norm_*); their
-backward keeps no statistics, it forms them again from x (h).  Argument
-marshalling only: both passes are the library's
+backward keeps no statistics, it forms them again from x (h).  A backward
+pass captured into a HIP graph needs every earlier autograd graph of the same
+leaves gone (torch orders their gradients with the stream that those ran on,
+which a capture does not allow).  Argument marshalling only: both passes are the library's
 kernels, and CPU tensors are refused as in chunk_fwd.
 """
 import torch

@@ -356,7 +356,7 @@ __global__ __launch_bounds__(CONV_STEP_THREADS) void conv_step_kernel(ConvStepAr
     for (int j = 0; j < W - 1; ++j) in[j] = *reinterpret_cast<const u32x4*>(state + (size_t)j * a.C);
     load(e.t0);
   }
-  if (e.bad || (a.update && a.b.slots && slot_repeats(a.b, seq, e.slot))) {
+  if (e.bad || (a.update && a.b.slots && slot_repeats<1>(a.b, seq, e.slot))) {
     float nan[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) nan[i] = __builtin_nanf("");

@@ -242,6 +242,7 @@ __global__ __launch_bounds__(NORM_THREADS) void gated_norm_bwd_kernel(GatedNormA
 #pragma unroll
     for (int j = 0; j < NORM_V; ++j) {
       float act = 1.f;
+      dact[j] = 0.f;
       if (a.gate) gate_act_d(g[j], a.act, act, dact[j]);
       e[j] *= a.scale;
       g[j] = act;

@@ -810,6 +810,8 @@ sf_status make_batch(int n_seq, int n_tok, int n_slots, const int* slots, const 
                      PoolBatch& b) {
   if (n_seq < 0 || n_tok < 0 || n_slots < 0)
     return fail(SF_ERR_INVALID_ARG, "n_seq, n_tok and n_slots must be >= 0");
+  // token indices run a staged chunk past the last one in 32 bits
+  if (n_tok > (1 << 30)) return fail(SF_ERR_UNSUPPORTED, "n_tok too large");
   if (!slots && n_slots < n_seq)
     return fail(SF_ERR_INVALID_ARG, "without slots the pool needs a slot per sequence");
   if (!seq_start && n_seq > 0 && n_tok % n_seq)
@@ -1046,9 +1048,9 @@ sf_status sf_gdn_gated_norm_bwd(const sf_gated_norm_shape* shape, const void* x,
   const size_t flat = (size_t)(a.N * row) * es;
   std::vector<Range> in = {{x, span(a.N, a.xs, row, es), "x"},
                            {gate, span(a.N, a.gs, row, es), "gate"},
-                           {w, (size_t)a.D * 4, "w"}, {dy, flat, "dy"},
-                           {workspace, ws_bytes, "workspace"}};
-  std::vector<Range> out = {{dx, flat, "dx"}, {dgate, flat, "dgate"}, {dw, (size_t)a.D * 4, "dw"}};
+                           {w, (size_t)a.D * 4, "w"}, {dy, flat, "dy"}};
+  std::vector<Range> out = {{dx, flat, "dx"}, {dgate, flat, "dgate"}, {dw, (size_t)a.D * 4, "dw"},
+                            {workspace, ws_bytes, "workspace"}};
   if ((s = check_ptrs(in, out, {})) != SF_OK) return s;
   const size_t need =
       dw ? align_up((size_t)gated_norm_groups(a.N, a.H, a.D) * a.D * 4) : 0;
@@ -1110,8 +1112,9 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
   if (ds && (!s || (a.N > 0 && !r))) return fail(SF_ERR_INVALID_ARG, "ds needs s and r");
   const size_t n = (size_t)(a.N * a.C) * es_of(shape->dtype), vec = (size_t)a.C * 4;
   std::vector<Range> in = {{h, n, "h"}, {r, n, "r"}, {s, vec, "s"}, {w, vec, "w"}, {dy, n, "dy"},
-                           {dh, n, "dh"}, {workspace, ws_bytes, "workspace"}};
-  std::vector<Range> out = {{dx, n, "dx"}, {dr, n, "dr"}, {dw, vec, "dw"}, {ds, vec, "ds"}};
+                           {dh, n, "dh"}};
+  std::vector<Range> out = {{dx, n, "dx"}, {dr, n, "dr"}, {dw, vec, "dw"}, {ds, vec, "ds"},
+                            {workspace, ws_bytes, "workspace"}};
   if ((st_ = check_ptrs(in, out, {})) != SF_OK) return st_;
   const size_t need = align_up((size_t)residual_norm_groups(a.N, a.C) * a.C * 4 *
                                ((dw ? 1 : 0) + (ds ? 1 : 0)));

@@ -32,6 +32,7 @@ def _step(n_seq=4, n_tok=4, n_slots=8, Hk=2, Hv=4, Dk=128, Dv=128, dtype=1, upda
     (dict(slots=None, n_slots=3), INV),             # fewer slots than sequences
     (dict(qs=64), INV), (dict(ks=260), INV), (dict(vs=-512), INV), (dict(vs=511), INV),
     (dict(n_seq=1 << 20, n_tok=1 << 20, Hk=1, Hv=4), UNS),
+    (dict(n_seq=1, n_tok=(1 << 30) + 1), UNS),
     (dict(q=None), INV), (dict(k=None), INV), (dict(v=None), INV), (dict(alpha=None), INV),
     (dict(beta=None), INV), (dict(state=None), INV), (dict(o=None), INV),
     (dict(q=G + 8), INV), (dict(state=8 * G + 4), INV), (dict(o=16 * G + 2), INV),
@@ -70,6 +71,7 @@ def _conv(n_seq=4, n_tok=4, n_slots=8, C=64, W=4, dtype=1, act=1, update=1, xs=0
     (dict(w=None), INV), (dict(state=None), INV), (dict(y=None), INV), (dict(x=G + 2), INV),
     (dict(y=G + 64), INV), (dict(state=6 * G + 16), INV), (dict(y=3 * G), INV),
     (dict(slots=5 * G + 64), INV),
+    (dict(n_seq=1 << 20, n_tok=1 << 20, C=4096), UNS), (dict(n_seq=1, n_tok=(1 << 30) + 1), UNS),
 ])
 def test_conv_step_refuses(kw, code):
     assert _conv(**kw) == code
@@ -109,7 +111,7 @@ def test_gated_norm_fwd_refuses(kw, code):
 @pytest.mark.parametrize("kw,code", SHAPES + [
     (dict(x=None), INV), (dict(dy=None), INV), (dict(dx=None), INV), (dict(gate=None), INV),
     (dict(dgate=None), INV), (dict(w=None), INV), (dict(dx=4 * G), INV), (dict(dgate=5 * G), INV),
-    (dict(dw=8 * G), INV), (dict(ws=None), WS), (dict(wsn=16), WS), (dict(ws=8 * G + 16), INV),
+    (dict(dw=8 * G), INV), (dict(ws=1 * G), INV), (dict(ws=None), WS), (dict(wsn=16), WS), (dict(ws=8 * G + 16), INV),
 ])
 def test_gated_norm_bwd_refuses(kw, code):
     assert _gbwd(**kw) == code
@@ -149,7 +151,7 @@ def test_residual_norm_fwd_refuses(kw, code):
 @pytest.mark.parametrize("kw,code", RSHAPES + [
     (dict(h=None), INV), (dict(dy=None), INV), (dict(dx=None), INV), (dict(w=None), INV),
     (dict(s=None), INV), (dict(r=None), INV), (dict(dx=6 * G), INV), (dict(dr=7 * G + 16), INV),
-    (dict(ds=11 * G), INV), (dict(ws=None), WS), (dict(wsn=1 << 16), WS),
+    (dict(ds=11 * G), INV), (dict(ws=6 * G), INV), (dict(ws=None), WS), (dict(wsn=1 << 16), WS),
     (dict(ws=11 * G + 128), INV),
 ])
 def test_residual_norm_bwd_refuses(kw, code):

@@ -166,6 +166,42 @@ def test_gated_norm_slices_of_wider_rows():
     assert y4.shape == (2, 20, H, D) and torch.equal(y4.view(40, H, D), y[:40])
 
 
+def test_offsets_past_32_bits():
+    """Tensors of 2^31 elements and a little more: their last rows, beyond
+    element 2^31, are those of a small call."""
+    N, H, D = (1 << 20) + 40, 16, 128
+    tail = 40
+    xs, gs, w, ds = [_c(t) for t in _gated(tail, H, D, "bf16", True, True, 10)]
+    big = []
+    for t in (xs, gs, ds):
+        b = torch.zeros(N, H, D, dtype=torch.bfloat16, device="cuda")
+        b[N - tail:] = t
+        big.append(b)
+    x, g, dy = big
+    assert (N - tail) * H * D >= 1 << 31
+    y = gdn.gated_norm_fwd(x, g, w)
+    dx, dg, dw = gdn.gated_norm_bwd(x, g, w, dy)
+    ref = gdn.gated_norm_bwd(xs, gs, w, ds)
+    torch.cuda.synchronize()
+    assert torch.equal(y[N - tail:], gdn.gated_norm_fwd(xs, gs, w))
+    assert torch.equal(dx[N - tail:], ref[0]) and torch.equal(dg[N - tail:], ref[1])
+    assert torch.allclose(dw, ref[2], rtol=1e-4, atol=1e-4)  # other rows add zeros, in another order
+    assert torch.count_nonzero(y[:1000]) == 0 and torch.count_nonzero(dx[N - 2000:N - tail]) == 0
+    del y, dx, dg
+    C = H * D
+    X, R, DY = (t.view(N, C) for t in (x, g, dy))
+    W = torch.linspace(0.5, 1.5, C, device="cuda")
+    y, h = gdn.residual_norm_fwd(X, R, W, W)
+    sy, sh = gdn.residual_norm_fwd(X[N - tail:], R[N - tail:], W, W)
+    assert torch.equal(y[N - tail:], sy) and torch.equal(h[N - tail:], sh)
+    del y
+    got = gdn.residual_norm_bwd(h, R, W, W, DY, X)
+    ref = gdn.residual_norm_bwd(sh, R[N - tail:], W, W, DY[N - tail:], X[N - tail:])
+    torch.cuda.synchronize()
+    assert torch.equal(got[0][N - tail:], ref[0]) and torch.equal(got[1][N - tail:], ref[1])
+    assert torch.count_nonzero(got[0][:1000]) == 0
+
+
 def test_no_rows():
     x = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(64, device="cuda")

@@ -97,6 +97,80 @@ def test_step_token_by_token_equals_one_call():
     assert torch.equal(c["state"], state)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 9])
+def test_step_bits_do_not_depend_on_the_batch(T, dtype):
+    """A sequence alone, in a batch of 40, and in one of 140 (whose 147 MB of
+    states go past the caches): the same outputs and state, to the bit."""
+    H, D = 16, 128
+    g = torch.Generator(device="cuda").manual_seed(81)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda")
+    n = 140
+    q, k = (torch.nn.functional.normalize(rnd(n, T, H, D), dim=-1).to(DT[dtype]) for _ in range(2))
+    v, al, be = rnd(n, T, H, D).to(DT[dtype]), rnd(n, T, H).sigmoid(), rnd(n, T, H).sigmoid()
+    pool = rnd(n, H, D, D)
+    flat = lambda t, m: t[:m].reshape(m * T, *t.shape[2:]).contiguous()
+    out = []
+    for m in (1, 40, n):
+        S = pool[:m].clone()
+        o = gdn.recurrent_step(*(flat(t, m) for t in (q, k, v, al, be)), S)
+        out.append((o[:T], S[0]))
+    torch.cuda.synchronize()
+    for o, S in out[1:]:
+        assert torch.equal(o, out[0][0]) and torch.equal(S, out[0][1])
+
+
+@pytest.mark.parametrize("n", [3, 300, 700])
+def test_repeated_slots_in_large_batches(n):
+    """The last entry repeats the first one's slot, one in the middle its
+    neighbour's: refused, and the others as without them."""
+    H, D, C = 1, 64, 64
+    lens = [1] * n
+    d = step_inputs(lens, H, H, D, "f32", n, seed=n)
+    ok, state_ok = _run(d)
+    cg = torch.Generator().manual_seed(n)
+    x, w = torch.randn(n, C, generator=cg).cuda(), torch.randn(C, 4, generator=cg).cuda()
+    cst = torch.randn(n, 3, C, generator=cg)
+    y_ok = gdn.shortconv_step(x, w, cst.cuda(), d["slots"].cuda())
+    keep = d["slots"].clone()
+    twice = {n - 1: 0, n // 2: n // 2 - 1}
+    for i, j in twice.items():
+        d["slots"][i] = keep[j]
+    o, state = _run(d)
+    pool = cst.cuda()
+    y = gdn.shortconv_step(x, w, pool, d["slots"].cuda())
+    torch.cuda.synchronize()
+    good = [i for i in range(n) if i not in twice]
+    assert torch.equal(o[good], ok[good]) and torch.equal(y[good], y_ok[good])
+    assert torch.isnan(o[list(twice)]).all() and torch.isnan(y[list(twice)]).all()
+    at = keep[good].long()
+    assert torch.equal(state[at], state_ok[at])
+    left = keep[list(twice)].long()  # slots that no entry names any more
+    assert torch.equal(state.cpu()[left], d["state"][left])
+    assert torch.equal(pool.cpu()[left], cst[left])
+
+
+def test_two_calls_at_once():
+    """Two streams, two pools, at the same time: as one after the other."""
+    a = _cuda(step_inputs([3] * 30, 4, 4, 128, "bf16", 30, seed=91))
+    b = _cuda(step_inputs([2] * 50, 4, 4, 128, "bf16", 50, seed=92))
+    call = lambda c, s, st: gdn.recurrent_step(c["q"], c["k"], c["v"], c["alpha"], c["beta"], s,
+                                               c["slots"], c["seq_start"], stream=st)
+    want = []
+    for c in (a, b):
+        s = c["state"].clone()
+        want += [call(c, s, None), s]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for c, st in zip((a, b), streams):
+        s = c["state"].clone()
+        st.wait_stream(torch.cuda.current_stream())
+        got += [call(c, s, st), s]
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+
+
 def test_step_strided_rows():
     """q, k and v as slices of one projection's rows."""
     lens = [2, 7, 1]
