@@ -305,29 +305,30 @@ __global__ __launch_bounds__(CONV_THREADS) void conv_dw_reduce_kernel(const floa
 // channels of one sequence, which it walks in runs of CONV_STEP_RUN tokens
 // whose loads are issued together, a run ahead (the first one's beside the
 // state's), so that a decoding step waits for memory twice: for the batch's
-// entry, and for all of its inputs.
+// entry, and for all of its inputs.  That latency is what bounds it: 256
+// sequences of 1 to 4 tokens and 6144 channels in bf16 (34.7 MB) take 8.9 us,
+// 19.2 with one token's loads at a time; one sequence of one token 2.2 us.
+// Four channels in bf16 as well, for more waves: eight took 10.4 us there and
+// 15.0 against 10.0 for 16 sequences of 30 tokens, two 8.9 and 7.9, but 3.45
+// against 3.21 for 64 sequences of one.  (The taps by way of LDS, for whole
+// lines: no gain.)
 constexpr int CONV_STEP_THREADS = 64;
 constexpr int CONV_STEP_RUN = 4;
+constexpr int CONV_STEP_V = 4;
 
 // Channel values as whole words: selects and loop-carried copies of them cost
 // a register per word.
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
-template <typename T, int V> __device__ __forceinline__ void unpack(u32x4 r, float (&f)[V]);
-template <> __device__ __forceinline__ void unpack<bf16, 8>(u32x4 r, float (&f)[8]) {
+template <typename T, int V> using Words = unsigned __attribute__((ext_vector_type(sizeof(T) * V / 4)));
+template <typename T, int V>
+__device__ __forceinline__ void unpack(Words<T, V> r, float (&f)[V]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[2 * i] = __uint_as_float(r[i] << 16);
-    f[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-  }
-}
-template <> __device__ __forceinline__ void unpack<float, 4>(u32x4 r, float (&f)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < V; ++i)
+    f[i] = __uint_as_float(sizeof(T) == 4 ? r[i] : i % 2 ? r[i / 2] & 0xffff0000u : r[i / 2] << 16);
 }
 
 template <typename T, int W, int V>
 __global__ __launch_bounds__(CONV_STEP_THREADS) void conv_step_kernel(ConvStepArgs a, int groups) {
-  static_assert(sizeof(T) * V == 16, "16 bytes of channels per thread");
+  typedef Words<T, V> words;
   constexpr int R = CONV_STEP_RUN;
   const int seq = blockIdx.x / groups;
   const int c0 = ((blockIdx.x - seq * groups) * CONV_STEP_THREADS + threadIdx.x) * V;
@@ -343,17 +344,17 @@ __global__ __launch_bounds__(CONV_STEP_THREADS) void conv_step_kernel(ConvStepAr
   T* __restrict__ y = reinterpret_cast<T*>(a.y) + c;
   const T* __restrict__ x = reinterpret_cast<const T*>(a.x) + c;
   T* state = reinterpret_cast<T*>(a.state);
-  u32x4 in[W - 1 + R];  // the W-1 inputs before a run, then the run
-  u32x4 nx[R];          // the next run
+  words in[W - 1 + R];  // the W-1 inputs before a run, then the run
+  words nx[R];          // the next run
   auto load = [&](int t) {
 #pragma unroll
     for (int r = 0; r < R; ++r)
-      if (t + r < e.t1) nx[r] = *reinterpret_cast<const u32x4*>(x + (size_t)(t + r) * a.xs);
+      if (t + r < e.t1) nx[r] = *reinterpret_cast<const words*>(x + (size_t)(t + r) * a.xs);
   };
   if (!e.bad) {
     state += (size_t)e.slot * (W - 1) * a.C + c;
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) in[j] = *reinterpret_cast<const u32x4*>(state + (size_t)j * a.C);
+    for (int j = 0; j < W - 1; ++j) in[j] = *reinterpret_cast<const words*>(state + (size_t)j * a.C);
     load(e.t0);
   }
   if (e.bad || (a.update && a.b.slots && slot_repeats<1>(a.b, seq, e.slot))) {
@@ -388,7 +389,7 @@ __global__ __launch_bounds__(CONV_STEP_THREADS) void conv_step_kernel(ConvStepAr
     // the last W-1 inputs up to token t + n - 1
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-      u32x4 p = in[j + 1];
+      words p = in[j + 1];
 #pragma unroll
       for (int m = 2; m <= R; ++m) p = n == m ? in[j + m] : p;
       in[j] = p;
@@ -396,7 +397,7 @@ __global__ __launch_bounds__(CONV_STEP_THREADS) void conv_step_kernel(ConvStepAr
   }
   if (a.update && live) {
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<u32x4*>(state + (size_t)j * a.C) = in[j];
+    for (int j = 0; j < W - 1; ++j) *reinterpret_cast<words*>(state + (size_t)j * a.C) = in[j];
   }
 }
 
@@ -488,7 +489,7 @@ hipError_t launch_conv_bwd(const ConvArgs& a, int GR, float* dwp, hipStream_t st
 
 template <typename T, int W>
 static hipError_t conv_step_w(const ConvStepArgs& a, hipStream_t st, Profiler* prof) {
-  constexpr int V = conv_vf<T>();
+  constexpr int V = CONV_STEP_V;
   const int gx = (a.C / V + CONV_STEP_THREADS - 1) / CONV_STEP_THREADS;
   prof_begin(prof, "conv_step", st);
   hipLaunchKernelGGL((conv_step_kernel<T, W, V>), dim3((unsigned)gx * a.b.n_seq),

@@ -12,6 +12,12 @@
 // pieces so that a load instruction of a wave covers 128 consecutive bytes of
 // eight rows), the two dot products end in three DPP steps among those lanes,
 // and the state stays in registers over all of a sequence's tokens.
+//
+// One token per sequence is bound by the states' traffic: 256 sequences of 32
+// value heads at D = 128 (1.08 GB) take 182 us, 5.9 TB/s; a plain device copy
+// of 1 GiB runs at 5.1 TB/s.  64 sequences of 1 to 8 tokens and 16 heads (139
+// MB) take 27 us, 5.1 TB/s.  A long run is bound by a token's dependent
+// arithmetic, 0.25 us: one sequence of 256 tokens takes 65 us.
 #pragma once
 #include "gdn_kernels.hpp"
 
