@@ -457,12 +457,14 @@ def _device_of(t, name):
     return t.device
 
 
-def _empty(like, shape):
-    """A contiguous tensor of `shape`, in the type and on the device of `like`
+def _new(like, shape, stream):
+    """A contiguous output of `shape`, in the type and on the device of `like`
     (empty_like is the cheaper call)."""
-    if like.shape == shape and like.is_contiguous():
-        return torch.empty_like(like)
-    return torch.empty(shape, dtype=like.dtype, device=like.device)
+    t = (torch.empty_like(like) if like.is_contiguous() and like.shape == shape else
+         torch.empty(shape, dtype=like.dtype, device=like.device))
+    if stream is not None:
+        used_on(stream, t)
+    return t
 
 
 @functools.lru_cache(maxsize=4096)
@@ -529,15 +531,19 @@ def _dtype_code(t, name):
 
 def _batch(slots, seq_start, n_slots, dev):
     """n_seq of a batch over a pool."""
-    n_seq = None
-    for t, n, extra in ((slots, "slots", 0), (seq_start, "seq_start", 1)):
-        if t is None:
-            continue
-        if t.dim() != 1 or t.shape[0] < extra:
-            raise ValueError("%s must have one dimension, of n_seq%s" % (n, " + 1" if extra else ""))
-        _need(t, n, torch.int32, (t.shape[0] if n_seq is None else n_seq + extra,), dev)
-        n_seq = t.shape[0] - extra
-    return n_slots if n_seq is None else n_seq
+    if slots is None and seq_start is None:
+        return n_slots
+    if slots is not None:
+        n_seq = slots.shape[0] if slots.dim() == 1 else -1
+        _need(slots, "slots", torch.int32, (n_seq,), dev)
+        if seq_start is None:
+            return n_seq
+    else:
+        n_seq = seq_start.shape[0] - 1 if seq_start.dim() == 1 else -1
+    if n_seq < 0:
+        raise ValueError("seq_start must be one-dimensional, n_seq + 1 offsets")
+    _need(seq_start, "seq_start", torch.int32, (n_seq + 1,), dev)
+    return n_seq
 
 
 def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=None, update=True,
@@ -552,25 +558,26 @@ def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=No
     every slot; negative: padding), seq_start [n_seq + 1] int32 its token rows
     (None: n_tok / n_seq each).  Returns o [n_tok, Hv, Dv]; rows of padding
     and past the last sequence keep what o held (pass o to set it)."""
-    dev = _device_of(q, "q")
+    dev, dt = _device_of(q, "q"), q.dtype
+    code = _dtype_code(q, "q")
     if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
         raise ValueError("q and v must be [n_tok, heads, D], state [n_slots, Hv, Dv, Dk]")
-    N, Hk, Dk = q.shape
-    Hv, Dv = v.shape[1:]
-    code = _dtype_code(q, "q")
-    qs = _token_rows(q, "q", q.dtype, (N, Hk, Dk), dev)
-    ks = _token_rows(k, "k", q.dtype, (N, Hk, Dk), dev)
-    vs = _token_rows(v, "v", q.dtype, (N, Hv, Dv), dev)
-    _need(alpha, "alpha", torch.float32, (N, Hv), dev)
-    _need(beta, "beta", torch.float32, (N, Hv), dev)
-    _need(state, "state", torch.float32, (state.shape[0], Hv, Dv, Dk), dev)
-    n_seq = _batch(slots, seq_start, state.shape[0], dev)
+    rows = N, Hk, Dk = q.shape
+    _, Hv, Dv = v.shape
+    n_slots = state.shape[0]
+    qs = _token_rows(q, "q", dt, rows, dev)
+    ks = _token_rows(k, "k", dt, rows, dev)
+    vs = _token_rows(v, "v", dt, (N, Hv, Dv), dev)
+    gates = (N, Hv)
+    _need(alpha, "alpha", torch.float32, gates, dev)
+    _need(beta, "beta", torch.float32, gates, dev)
+    _need(state, "state", torch.float32, (n_slots, Hv, Dv, Dk), dev)
+    n_seq = _batch(slots, seq_start, n_slots, dev)
     if o is None:
-        o = _empty(v, (N, Hv, Dv))
-        used_on(stream, o)
+        o = _new(v, (N, Hv, Dv), stream)
     else:
-        _need(o, "o", q.dtype, (N, Hv, Dv), dev)
-    shape = _shape_ref(StepShape, n_seq, N, state.shape[0], Hk, Hv, Dk, Dv, code,
+        _need(o, "o", dt, (N, Hv, Dv), dev)
+    shape = _shape_ref(StepShape, n_seq, N, n_slots, Hk, Hv, Dk, Dv, code,
                        1 if update else 0, qs, ks, vs)
     _run("sf_gdn_recurrent_step", dev, stream, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(),
          alpha.data_ptr(), beta.data_ptr(), _addr(slots), _addr(seq_start), state.data_ptr(),
@@ -597,8 +604,7 @@ def shortconv_step(x, w, state, slots=None, seq_start=None, act=0, y=None, updat
     _need(state, "state", x.dtype, (state.shape[0], W - 1, C), dev)
     n_seq = _batch(slots, seq_start, state.shape[0], dev)
     if y is None:
-        y = _empty(x, (N, C))
-        used_on(stream, y)
+        y = _new(x, (N, C), stream)
     else:
         _need(y, "y", x.dtype, (N, C), dev)
     shape = _shape_ref(ConvStepShape, n_seq, N, state.shape[0], C, W, code, int(act),
@@ -664,8 +670,7 @@ def gated_norm_fwd(x, gate=None, w=None, eps=1e-6, scale=1.0, act=1, y=None, str
     if w is not None:
         _need(w, "w", torch.float32, (x.shape[2],), dev)
     if y is None:
-        y = _empty(x, full)
-        used_on(stream, y)
+        y = _new(x, full, stream)
     else:
         _need(y, "y", x.dtype, full, dev)
     _run("sf_gdn_gated_norm_fwd", dev, stream, shape, x.data_ptr(), _addr(gate), _addr(w),
@@ -731,26 +736,25 @@ def residual_norm_fwd(x, r=None, w=None, s=None, scale=1.0, eps=1e-6, h=None, y=
     (None: ones).  Returns (y, h)."""
     dev = _device_of(x, "x")
     shape = _shape_ref(ResidualNormShape, *_residual_norm_fields(x, eps, scale))
-    _need(x, "x", x.dtype, x.shape, dev)
-    vec = x.shape[-1:]
+    full = x.shape
+    _need(x, "x", x.dtype, full, dev)
+    vec = full[-1:]
     if w is not None:
         _need(w, "w", torch.float32, vec, dev)
     if s is not None:
         _need(s, "s", torch.float32, vec, dev)
     if r is not None:
-        _need(r, "r", x.dtype, x.shape, dev)
+        _need(r, "r", x.dtype, full, dev)
         if h is None:
-            h = torch.empty_like(x)
-            used_on(stream, h)
+            h = _new(x, full, stream)
         else:
-            _need(h, "h", x.dtype, x.shape, dev)
+            _need(h, "h", x.dtype, full, dev)
     elif s is not None or h is not None:
         raise ValueError("s and h need r")
     if y is None:
-        y = torch.empty_like(x)
-        used_on(stream, y)
+        y = _new(x, full, stream)
     else:
-        _need(y, "y", x.dtype, x.shape, dev)
+        _need(y, "y", x.dtype, full, dev)
     _run("sf_gdn_residual_norm_fwd", dev, stream, shape, x.data_ptr(), _addr(r), _addr(s),
          _addr(w), _addr(h), y.data_ptr())
     return y, (x if r is None else h)
