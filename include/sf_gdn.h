@@ -271,7 +271,9 @@ typedef struct {
  * sf_gdn_chunk_fwd, in fp32 throughout (o is rounded once); a chunk's S_out
  * of one sequence is a pool slot.  Meant for the few tokens per sequence of a
  * decoding step: every token costs a pass over the state in registers, so
- * long prompts belong to the chunk calls.
+ * long prompts belong to the chunk calls.  A sequence's outputs and state are
+ * the same, bit for bit, whatever else is in the batch and however its tokens
+ * are spread over calls.
  *   q, k [n_tok, Hk, Dk], v [n_tok, Hv, Dv], o [n_tok, Hv, Dv]  dtype
  *   alpha, beta [n_tok, Hv] fp32 (4-byte aligned)
  *   state [n_slots, Hv, Dv, Dk] fp32, in place. */

@@ -153,7 +153,7 @@ __device__ __forceinline__ void gate_act_d(float g, int act, float& a, float& d)
 __device__ __forceinline__ size_t head_row(unsigned i, const GatedNormArgs& a, long long ts) {
   if (ts == (long long)a.H * a.D) return (size_t)i * a.D;
   const unsigned n = i / (unsigned)a.H;
-  return (size_t)n * ts + (size_t)((i - n * a.H) * a.D);
+  return (size_t)n * ts + (size_t)(i - n * a.H) * a.D;
 }
 
 template <typename T, int L, bool STREAM>
