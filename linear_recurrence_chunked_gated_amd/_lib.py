@@ -618,7 +618,21 @@ def _heads(x):
     """[N, H, D] view of x [..., H, D] (no copy)."""
     if x.dim() < 3:
         raise ValueError("expected [..., H, D], got shape %s" % (tuple(x.shape),))
-    return x if x.dim() == 3 else x.view(-1, x.shape[-2], x.shape[-1])
+    if x.dim() == 3:
+        return x
+    try:
+        return x.view(-1, x.shape[-2], x.shape[-1])
+    except RuntimeError:
+        raise ValueError("the rows of all leading dimensions must lie at one stride, got strides "
+                         "%s of shape %s" % (x.stride(), tuple(x.shape))) from None
+
+
+def _gate_rows(gate, full):
+    if gate is None:
+        return None
+    if gate.shape != full:
+        raise ValueError("gate has shape %s, expected %s" % (tuple(gate.shape), tuple(full)))
+    return _heads(gate)
 
 
 def _gated_norm_fields(x, gate, eps, scale, act):
@@ -664,7 +678,7 @@ def gated_norm_fwd(x, gate=None, w=None, eps=1e-6, scale=1.0, act=1, y=None, str
     rows."""
     full = x.shape
     x = _heads(x)
-    gate = None if gate is None else _heads(gate)
+    gate = _gate_rows(gate, full)
     shape = _shape_ref(GatedNormShape, *_gated_norm_fields(x, gate, eps, scale, act))
     dev = x.device
     if w is not None:
@@ -685,7 +699,7 @@ def gated_norm_bwd(x, gate, w, dy, eps=1e-6, scale=1.0, act=1, grads=None, want_
     ``grads`` may supply preallocated outputs in that order."""
     full = x.shape
     x = _heads(x)
-    gate = None if gate is None else _heads(gate)
+    gate = _gate_rows(gate, full)
     fields = _gated_norm_fields(x, gate, eps, scale, act)
     dev, D = x.device, x.shape[2]
     if w is not None:

@@ -791,6 +791,14 @@ sf_status sf_gdn_shortconv_bwd(const sf_conv_shape* shape, const void* x, const 
 // ------------------------------------------------ single tokens over a pool
 namespace {
 
+// What an entry point returns where the host's memory ran out under its
+// checks: nothing is thrown across the ABI.  (The text fits a string that
+// allocates nothing.)
+sf_status host_failure() noexcept {
+  g_err = "out of memory";
+  return SF_ERR_HIP;
+}
+
 sf_status check_ints(const int* p, const char* name) {
   if ((uintptr_t)p % 4) return fail(SF_ERR_INVALID_ARG, std::string(name) + " is not 4-byte aligned");
   return SF_OK;
@@ -856,7 +864,7 @@ extern "C" {
 sf_status sf_gdn_recurrent_step(const sf_step_shape* shape, const void* q, const void* k,
                                 const void* v, const float* alpha, const float* beta,
                                 const int* slots, const int* seq_start, float* state, void* o,
-                                void* stream) {
+                                void* stream) try {
   if (!shape) return fail(SF_ERR_INVALID_ARG, "shape is NULL");
   const sf_step_shape& p = *shape;
   sf_status s;
@@ -907,11 +915,13 @@ sf_status sf_gdn_recurrent_step(const sf_step_shape* shape, const void* q, const
     if (e != hipSuccess) return hip_fail(e, "recurrent step launch");
     return SF_OK;
   });
+} catch (...) {
+  return host_failure();
 }
 
 sf_status sf_gdn_shortconv_step(const sf_conv_step_shape* shape, const void* x, const float* w,
                                 const int* slots, const int* seq_start, void* state, void* y,
-                                void* stream) {
+                                void* stream) try {
   if (!shape) return fail(SF_ERR_INVALID_ARG, "shape is NULL");
   const sf_conv_step_shape& p = *shape;
   sf_status s;
@@ -947,6 +957,8 @@ sf_status sf_gdn_shortconv_step(const sf_conv_step_shape* shape, const void* x, 
     if (e != hipSuccess) return hip_fail(e, "convolution step launch");
     return SF_OK;
   });
+} catch (...) {
+  return host_failure();
 }
 
 }  // extern "C"
@@ -1001,7 +1013,7 @@ sf_status check_norm_ws(size_t need, const void* workspace, size_t ws_bytes) {
 extern "C" {
 
 sf_status sf_gdn_gated_norm_fwd(const sf_gated_norm_shape* shape, const void* x, const void* gate,
-                                const float* w, void* y, void* stream) {
+                                const float* w, void* y, void* stream) try {
   GatedNormArgs a{};
   sf_status s = make_gated(shape, a);
   if (s != SF_OK) return s;
@@ -1022,20 +1034,24 @@ sf_status sf_gdn_gated_norm_fwd(const sf_gated_norm_shape* shape, const void* x,
     if (e != hipSuccess) return hip_fail(e, "gated norm launch");
     return SF_OK;
   });
+} catch (...) {
+  return host_failure();
 }
 
-sf_status sf_gdn_gated_norm_bwd_workspace_size(const sf_gated_norm_shape* shape, size_t* bytes) {
+sf_status sf_gdn_gated_norm_bwd_workspace_size(const sf_gated_norm_shape* shape, size_t* bytes) try {
   GatedNormArgs a{};
   sf_status s = make_gated(shape, a);
   if (s != SF_OK) return s;
   if (!bytes) return fail(SF_ERR_INVALID_ARG, "bytes is NULL");
   *bytes = align_up((size_t)gated_norm_groups(a.N, a.H, a.D) * a.D * 4);
   return SF_OK;
+} catch (...) {
+  return host_failure();
 }
 
 sf_status sf_gdn_gated_norm_bwd(const sf_gated_norm_shape* shape, const void* x, const void* gate,
                                 const float* w, const void* dy, void* dx, void* dgate, float* dw,
-                                void* workspace, size_t ws_bytes, void* stream) {
+                                void* workspace, size_t ws_bytes, void* stream) try {
   GatedNormArgs a{};
   sf_status s = make_gated(shape, a);
   if (s != SF_OK) return s;
@@ -1064,11 +1080,13 @@ sf_status sf_gdn_gated_norm_bwd(const sf_gated_norm_shape* shape, const void* x,
     if (e != hipSuccess) return hip_fail(e, "gated norm launch");
     return SF_OK;
   });
+} catch (...) {
+  return host_failure();
 }
 
 sf_status sf_gdn_residual_norm_fwd(const sf_residual_norm_shape* shape, const void* x,
                                    const void* r, const float* s, const float* w, void* h, void* y,
-                                   void* stream) {
+                                   void* stream) try {
   ResidualNormArgs a{};
   sf_status st_ = make_residual(shape, a);
   if (st_ != SF_OK) return st_;
@@ -1088,22 +1106,26 @@ sf_status sf_gdn_residual_norm_fwd(const sf_residual_norm_shape* shape, const vo
     if (e != hipSuccess) return hip_fail(e, "residual norm launch");
     return SF_OK;
   });
+} catch (...) {
+  return host_failure();
 }
 
 sf_status sf_gdn_residual_norm_bwd_workspace_size(const sf_residual_norm_shape* shape,
-                                                  size_t* bytes) {
+                                                  size_t* bytes) try {
   ResidualNormArgs a{};
   sf_status s = make_residual(shape, a);
   if (s != SF_OK) return s;
   if (!bytes) return fail(SF_ERR_INVALID_ARG, "bytes is NULL");
   *bytes = align_up((size_t)residual_norm_groups(a.N, a.C) * a.C * 4 * 2);
   return SF_OK;
+} catch (...) {
+  return host_failure();
 }
 
 sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const void* h,
                                    const void* r, const float* s, const float* w, const void* dy,
                                    const void* dh, void* dx, void* dr, float* dw, float* ds,
-                                   void* workspace, size_t ws_bytes, void* stream) {
+                                   void* workspace, size_t ws_bytes, void* stream) try {
   ResidualNormArgs a{};
   sf_status st_ = make_residual(shape, a);
   if (st_ != SF_OK) return st_;
@@ -1129,6 +1151,8 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
     if (e != hipSuccess) return hip_fail(e, "residual norm launch");
     return SF_OK;
   });
+} catch (...) {
+  return host_failure();
 }
 
 }  // extern "C"

@@ -202,6 +202,26 @@ def test_offsets_past_32_bits():
     assert torch.count_nonzero(got[0][:1000]) == 0
 
 
+def test_more_rows_than_a_launch_holds():
+    """Rows past the largest grid are taken in a second turn."""
+    N, tail = (1 << 21) * 32 + 50, 60
+    x, g, w, _ = [_c(t) for t in _gated(tail, 1, 8, "bf16", True, True, 11)]
+    X = torch.zeros(N, 1, 8, dtype=torch.bfloat16, device="cuda")
+    X[N - tail:] = x
+    G = torch.zeros_like(X)
+    G[N - tail:] = g
+    y = gdn.gated_norm_fwd(X, G, w)
+    torch.cuda.synchronize()
+    assert torch.equal(y[N - tail:], gdn.gated_norm_fwd(x, g, w))
+    assert torch.count_nonzero(y[:N - tail]) == 0
+    X, G, y = X.view(-1, 8), G.view(-1, 8), None
+    y, h = gdn.residual_norm_fwd(X, G, w)
+    sy, sh = gdn.residual_norm_fwd(x.view(-1, 8), g.view(-1, 8), w)
+    torch.cuda.synchronize()
+    assert torch.equal(y[N - tail:], sy) and torch.equal(h[N - tail:], sh)
+    assert torch.count_nonzero(y[:N - tail]) == 0
+
+
 def test_no_rows():
     x = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda")
     w = torch.ones(64, device="cuda")
@@ -338,6 +358,8 @@ def test_binding_refusals():
             (TypeError, lambda: gdn.gated_norm_fwd(x, x.bfloat16())),
             (ValueError, lambda: gdn.gated_norm_fwd(x, x[:2])),
             (ValueError, lambda: gdn.gated_norm_fwd(x, None, w[:32])),
+            (ValueError, lambda: gdn.gated_norm_fwd(x.view(2, 2, 2, 64), x)),
+            (ValueError, lambda: gdn.gated_norm_fwd(x.view(2, 2, 2, 64).transpose(0, 1))),
             (ValueError, lambda: gdn.gated_norm_fwd(x.transpose(0, 1))),
             (ValueError, lambda: gdn.gated_norm_fwd(w)),
             (ValueError, lambda: gdn.gated_norm_bwd(x, None, w, x[:, :1])),

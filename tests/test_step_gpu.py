@@ -390,6 +390,26 @@ def test_steps_replay_from_a_graph_and_on_a_side_stream():
         for got, ref in zip((o, y, pool, cpool), want[rep]):
             assert torch.equal(got, ref), rep
 
+    # another batch by writing its arrays: other slots, other lengths, padding
+    c2 = {n: t.clone() for n, t in c.items()}
+    c2["slots"] = torch.tensor([5, -1, 0, 2], dtype=torch.int32).cuda()
+    c2["seq_start"] = torch.tensor([0, 3, 3, 5, 6], dtype=torch.int32).cuda()
+    mark = lambda t: t.fill_(3.0)
+    o2, y2, pool2, cpool2 = mark(torch.empty_like(o)), mark(torch.empty_like(y)), pool.clone(), \
+        cpool.clone()
+    _decode(d, c2, pool2, cpool2, x, w, o2, y2)
+    c["slots"].copy_(c2["slots"])
+    old = c["seq_start"].clone()
+    c["seq_start"].copy_(c2["seq_start"])
+    mark(o), mark(y)
+    graph.replay()
+    torch.cuda.synchronize()
+    for got, ref in zip((o, y, pool, cpool), (o2, y2, pool2, cpool2)):
+        assert torch.equal(got, ref)
+    assert (o[6] == 3.0).all() and (y[6] == 3.0).all()  # a row of no sequence
+    c["slots"].copy_(d["slots"])
+    c["seq_start"].copy_(old)
+
     side = torch.cuda.Stream()
     pool = c["state"].clone()
     side.wait_stream(torch.cuda.current_stream())
