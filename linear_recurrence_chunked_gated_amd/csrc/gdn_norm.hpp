@@ -130,7 +130,7 @@ __device__ __forceinline__ float rstd_of(float sum2, float inv_n, float eps) {
 // sigmoid(g) in the hardware's exponential and reciprocal (an ulp each, the
 // exponent's rounding |g| ulps / 2): the library forms' range handling and
 // exact division cost twice the rest of the norm, and the ends are right as
-// they are (exp(-g) = inf gives 0).
+// they are (exp(-g) = inf gives 0, and what is below 2^-126 may become 0).
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
 }
@@ -254,7 +254,8 @@ __global__ __launch_bounds__(NORM_THREADS) void gated_norm_bwd_kernel(GatedNormA
       g[j] = act;
       t[j] = e[j] * w[j] * act;
     }
-    const float rstd = rstd_of(sum_lanes<L>(dot8(x, x)), inv_d, a.eps);
+    float rstd = rstd_of(sum_lanes<L>(dot8(x, x)), inv_d, a.eps);
+    if (i >= M) rstd = 0.f;  // no row: with eps = 0 it would be infinite, and dw NaN
     const float m = rstd * sum_lanes<L>(dot8(t, x)) * inv_d;
     const bool live = i < M && col;
 #pragma unroll
@@ -541,7 +542,9 @@ __global__ __launch_bounds__(row_threads<L>()) void residual_norm_bwd_kernel(Res
       for (int j = 0; j < NORM_V; ++j) gn += dy[p][j] * w[p][j] * h[p][j];
     }
     row_sums<L>(ss, gn, lds[par]);
-    const float rstd = rstd_of(ss, inv_c, a.eps), m = rstd * gn * inv_c;
+    float rstd = rstd_of(ss, inv_c, a.eps);
+    if (i >= a.N) rstd = 0.f;  // no row: with eps = 0 it would be infinite, and dw NaN
+    const float m = rstd * gn * inv_c;
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       const int c = (p * L + l) * NORM_V;

@@ -166,6 +166,26 @@ def test_gated_norm_slices_of_wider_rows():
     assert y4.shape == (2, 20, H, D) and torch.equal(y4.view(40, H, D), y[:40])
 
 
+@pytest.mark.parametrize("N,C", [(1, 72), (5, 8), (3, 512), (2, 640)])
+def test_eps_zero_with_fewer_rows_than_a_workgroup_takes(N, C):
+    """The workgroup's places without a row add nothing to the weight
+    gradients, though 1 / sqrt(0 + 0) is infinite."""
+    gen = torch.Generator().manual_seed(N + C)
+    x, g, dy, dh = (torch.randn(N, C, generator=gen) for _ in range(4))
+    w, s = 1 + 0.3 * torch.randn(C, generator=gen), 1 + 0.3 * torch.randn(C, generator=gen)
+    if C <= 512:
+        kw = dict(eps=0.0, scale=1.0, act=1)
+        t = [v.view(N, 1, C) for v in (x, g, dy)]
+        got = gdn.gated_norm_bwd(_c(t[0]), _c(t[1]), _c(w), _c(t[2]), **kw)
+        refs, bounds = gated_norm_bwd_ref(t[0], t[1], w, t[2], depth=N + 64, **kw)
+        for name, a, b, e in zip(("dx", "dgate", "dw"), got, refs, bounds):
+            check(name, a, b, e, "f32")
+    got = gdn.residual_norm_bwd(_c(x), _c(g), _c(w), _c(s), _c(dy), _c(dh), eps=0.0)
+    refs, bounds = residual_norm_bwd_ref(x, g, w, s, dy, dh, 0.0, 1.0, depth=N + 64)
+    for name, a, b, e in zip(("dx", "dr", "dw", "ds"), got, refs, bounds):
+        check(name, a, b, e, "f32")
+
+
 def test_offsets_past_32_bits():
     """Tensors of 2^31 elements and a little more: their last rows, beyond
     element 2^31, are those of a small call."""
