@@ -2,10 +2,12 @@
 
 Argument marshalling only: torch provides device memory and the stream, and
 every step of the computation runs in the library's HIP kernels.  There is no
-fallback: if the library is missing or fails, calls raise.
+fallback: if the library is missing or fails, calls raise.  The decoding calls
+and the norms, whose kernels are shorter than their marshalling in Python,
+check and call through the native module _calls (csrc/sf_gdn_calls.cpp) on the
+same entry points.
 """
 import ctypes
-import functools
 import os
 
 import torch
@@ -197,9 +199,6 @@ def alloc_workspace(nbytes, device):
 
 
 def _need(t, name, dtype, shape, device):
-    if (t is not None and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
-        return
     if t is None:
         raise ValueError("%s is required" % name)
     if t.device != device:
@@ -451,99 +450,46 @@ def shortconv_bwd(x, w, conv_in, dy, dconv_out=None, act=0, dx=None, dw=None, wa
     return dx, dw, dci
 
 
-def _device_of(t, name):
+# ---- decoding and norms: checks, allocation and call in the native module ----
+_calls = None
+
+# The C entry points that _calls takes, in its order.
+_CALL_ENTRIES = ("sf_gdn_recurrent_step", "sf_gdn_shortconv_step", "sf_gdn_gated_norm_fwd",
+                 "sf_gdn_gated_norm_bwd", "sf_gdn_gated_norm_bwd_workspace_size",
+                 "sf_gdn_residual_norm_fwd", "sf_gdn_residual_norm_bwd",
+                 "sf_gdn_residual_norm_bwd_workspace_size")
+
+
+def _raise(status, where):
+    _check(status, where)
+
+
+def load_calls():
+    """The native module _calls, on the library's entry points (raises if
+    either has not been built)."""
+    global _calls
+    if _calls is None:
+        lib = load()
+        if not os.path.exists(os.path.join(_HERE, "_calls.so")):
+            raise RuntimeError("_calls.so is not built; run "
+                               "`python -m linear_recurrence_chunked_gated_amd.build`")
+        from . import _calls as module
+        module.bind(_raise, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                              for n in _CALL_ENTRIES))
+        _calls = module
+    return _calls
+
+
+def _raw_stream(t, stream):
+    """The stream handle for a call on t's device: the current stream there
+    when None."""
+    if stream is None and t.is_cuda:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
     if not t.is_cuda:
-        raise ValueError("tensors must be on a GPU device (%s is on %s)" % (name, t.device))
-    return t.device
-
-
-def _new(like, shape, stream):
-    """A contiguous output of `shape`, in the type and on the device of `like`
-    (empty_like is the cheaper call)."""
-    t = (torch.empty_like(like) if like.is_contiguous() and like.shape == shape else
-         torch.empty(shape, dtype=like.dtype, device=like.device))
-    if stream is not None:
-        used_on(stream, t)
-    return t
-
-
-@functools.lru_cache(maxsize=4096)
-def _shape_ref(cls, *fields):
-    """A shape structure, as the calls take it (they only read it)."""
-    return ctypes.byref(cls(*fields))
-
-
-def _addr(t):
-    return None if t is None else t.data_ptr()
-
-
-def _run(fn, dev, stream, *args):
-    """The call `fn` on `stream` (the current stream of `dev` when None), with
-    `dev` current, so that tensors of another device than the current one run
-    on their own."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(dev.index)
-    elif stream.device != dev:
-        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, dev))
-    else:
-        raw = stream.cuda_stream
-    call = getattr(_lib or load(), fn)
-    if torch._C._cuda_getDevice() == dev.index:
-        st = call(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            st = call(*args, raw)
-    if st != SF_OK:
-        _check(st, fn)
-
-
-def _token_rows(t, name, dtype, shape, device):
-    """Elements between the token rows of t [n, ...], whose rows are
-    contiguous but may lie apart (a slice of wider rows); 0 when there is at
-    most one."""
-    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
-        return 0
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if t.dtype != dtype:
-        raise TypeError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.is_contiguous() or t.shape[0] == 0:
-        return 0
-    strides, width = t.stride(), 1
-    for n, st in zip(reversed(t.shape[1:]), reversed(strides[1:])):
-        if n != 1 and st != width:
-            raise ValueError("%s: each token's row must be contiguous" % name)
-        width *= n
-    if t.shape[0] == 1:
-        return 0
-    if strides[0] < width:
-        raise ValueError("%s: token rows must not overlap" % name)
-    return strides[0]
-
-
-def _dtype_code(t, name):
-    if t.dtype not in _DTYPES:
-        raise TypeError("%s must be bfloat16 or float32, got %s" % (name, t.dtype))
-    return _DTYPES[t.dtype]
-
-
-def _batch(slots, seq_start, n_slots, dev):
-    """n_seq of a batch over a pool."""
-    if slots is None and seq_start is None:
-        return n_slots
-    if slots is not None:
-        n_seq = slots.shape[0] if slots.dim() == 1 else -1
-        _need(slots, "slots", torch.int32, (n_seq,), dev)
-        if seq_start is None:
-            return n_seq
-    else:
-        n_seq = seq_start.shape[0] - 1 if seq_start.dim() == 1 else -1
-    if n_seq < 0:
-        raise ValueError("seq_start must be one-dimensional, n_seq + 1 offsets")
-    _need(seq_start, "seq_start", torch.int32, (n_seq + 1,), dev)
-    return n_seq
+        raise ValueError("tensors must be on a GPU device, got one on %s" % t.device)
+    if stream.device != t.device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
+    return stream.cuda_stream
 
 
 def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=None, update=True,
@@ -558,31 +504,11 @@ def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=No
     every slot; negative: padding), seq_start [n_seq + 1] int32 its token rows
     (None: n_tok / n_seq each).  Returns o [n_tok, Hv, Dv]; rows of padding
     and past the last sequence keep what o held (pass o to set it)."""
-    dev, dt = _device_of(q, "q"), q.dtype
-    code = _dtype_code(q, "q")
-    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
-        raise ValueError("q and v must be [n_tok, heads, D], state [n_slots, Hv, Dv, Dk]")
-    rows = N, Hk, Dk = q.shape
-    _, Hv, Dv = v.shape
-    n_slots = state.shape[0]
-    qs = _token_rows(q, "q", dt, rows, dev)
-    ks = _token_rows(k, "k", dt, rows, dev)
-    vs = _token_rows(v, "v", dt, (N, Hv, Dv), dev)
-    gates = (N, Hv)
-    _need(alpha, "alpha", torch.float32, gates, dev)
-    _need(beta, "beta", torch.float32, gates, dev)
-    _need(state, "state", torch.float32, (n_slots, Hv, Dv, Dk), dev)
-    n_seq = _batch(slots, seq_start, n_slots, dev)
-    if o is None:
-        o = _new(v, (N, Hv, Dv), stream)
-    else:
-        _need(o, "o", dt, (N, Hv, Dv), dev)
-    shape = _shape_ref(StepShape, n_seq, N, n_slots, Hk, Hv, Dk, Dv, code,
-                       1 if update else 0, qs, ks, vs)
-    _run("sf_gdn_recurrent_step", dev, stream, shape, q.data_ptr(), k.data_ptr(), v.data_ptr(),
-         alpha.data_ptr(), beta.data_ptr(), _addr(slots), _addr(seq_start), state.data_ptr(),
-         o.data_ptr())
-    return o
+    got = (_calls or load_calls()).recurrent_step(q, k, v, alpha, beta, state, slots, seq_start, o,
+                                                  update, _raw_stream(q, stream))
+    if stream is not None and o is None:
+        used_on(stream, got)
+    return got
 
 
 def shortconv_step(x, w, state, slots=None, seq_start=None, act=0, y=None, update=True,
@@ -593,56 +519,11 @@ def shortconv_step(x, w, state, slots=None, seq_start=None, act=0, y=None, updat
     x [n_tok, C] (token rows may be slices of wider rows), w [C, W] fp32,
     state [n_slots, W-1, C] in x's dtype, advanced in place unless update is
     False; slots and seq_start as in recurrent_step.  Returns y [n_tok, C]."""
-    dev = _device_of(x, "x")
-    if x.dim() != 2 or w.dim() != 2 or state.dim() != 3:
-        raise ValueError("x must be [n_tok, C], w [C, W], state [n_slots, W-1, C]")
-    N, C = x.shape
-    W = w.shape[1]
-    code = _dtype_code(x, "x")
-    xs = _token_rows(x, "x", x.dtype, (N, C), dev)
-    _need(w, "w", torch.float32, (C, W), dev)
-    _need(state, "state", x.dtype, (state.shape[0], W - 1, C), dev)
-    n_seq = _batch(slots, seq_start, state.shape[0], dev)
-    if y is None:
-        y = _new(x, (N, C), stream)
-    else:
-        _need(y, "y", x.dtype, (N, C), dev)
-    shape = _shape_ref(ConvStepShape, n_seq, N, state.shape[0], C, W, code, int(act),
-                       1 if update else 0, xs)
-    _run("sf_gdn_shortconv_step", dev, stream, shape, x.data_ptr(), w.data_ptr(), _addr(slots),
-         _addr(seq_start), state.data_ptr(), y.data_ptr())
-    return y
-
-
-def _heads(x):
-    """[N, H, D] view of x [..., H, D] (no copy)."""
-    if x.dim() < 3:
-        raise ValueError("expected [..., H, D], got shape %s" % (tuple(x.shape),))
-    if x.dim() == 3:
-        return x
-    try:
-        return x.view(-1, x.shape[-2], x.shape[-1])
-    except RuntimeError:
-        raise ValueError("the rows of all leading dimensions must lie at one stride, got strides "
-                         "%s of shape %s" % (x.stride(), tuple(x.shape))) from None
-
-
-def _gate_rows(gate, full):
-    if gate is None:
-        return None
-    if gate.shape != full:
-        raise ValueError("gate has shape %s, expected %s" % (tuple(gate.shape), tuple(full)))
-    return _heads(gate)
-
-
-def _gated_norm_fields(x, gate, eps, scale, act):
-    """GatedNormShape's fields for x [N, H, D] and gate, which are checked."""
-    dev = _device_of(x, "x")
-    code = _dtype_code(x, "x")
-    full = N, H, D = x.shape
-    xs = _token_rows(x, "x", x.dtype, full, dev)
-    gs = 0 if gate is None else _token_rows(gate, "gate", x.dtype, full, dev)
-    return N, H, D, code, int(act), float(eps), float(scale), xs, gs
+    got = (_calls or load_calls()).shortconv_step(x, w, state, slots, seq_start, act, y, update,
+                                                  _raw_stream(x, stream))
+    if stream is not None and y is None:
+        used_on(stream, got)
+    return got
 
 
 def gated_norm_bwd_workspace_bytes(shape):
@@ -652,44 +533,17 @@ def gated_norm_bwd_workspace_bytes(shape):
     return n.value
 
 
-def _norm_workspace(query, cls, fields, workspace, dev, stream):
-    """The caller's workspace if it is large enough, else a new one."""
-    need = _norm_bytes(query, cls, *fields)
-    if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, (workspace.numel(),), dev)
-    if need > 0 and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if workspace.data_ptr() % 256:
-            workspace = alloc_workspace(need, dev)
-        used_on(stream, workspace)
-    return workspace
-
-
-@functools.lru_cache(maxsize=4096)
-def _norm_bytes(query, cls, *fields):
-    return query(cls(*fields))
-
-
 def gated_norm_fwd(x, gate=None, w=None, eps=1e-6, scale=1.0, act=1, y=None, stream=None):
     """sf_gdn_gated_norm_fwd on torch tensors: y = scale * w * x / sqrt(mean(
     x^2) + eps) * act(gate) over the last dimension of x [..., H, D], with
     gate like x or None (factor 1) and w [D] fp32 or None (ones); act 1 for
     SiLU, 0 for the gate itself.  x and gate may be head slices of wider token
     rows."""
-    full = x.shape
-    x = _heads(x)
-    gate = _gate_rows(gate, full)
-    shape = _shape_ref(GatedNormShape, *_gated_norm_fields(x, gate, eps, scale, act))
-    dev = x.device
-    if w is not None:
-        _need(w, "w", torch.float32, (x.shape[2],), dev)
-    if y is None:
-        y = _new(x, full, stream)
-    else:
-        _need(y, "y", x.dtype, full, dev)
-    _run("sf_gdn_gated_norm_fwd", dev, stream, shape, x.data_ptr(), _addr(gate), _addr(w),
-         y.data_ptr())
-    return y
+    got = (_calls or load_calls()).gated_norm_fwd(x, gate, w, eps, scale, act, y,
+                                                  _raw_stream(x, stream))
+    if stream is not None and y is None:
+        used_on(stream, got)
+    return got
 
 
 def gated_norm_bwd(x, gate, w, dy, eps=1e-6, scale=1.0, act=1, grads=None, want_dw=True,
@@ -697,42 +551,11 @@ def gated_norm_bwd(x, gate, w, dy, eps=1e-6, scale=1.0, act=1, grads=None, want_
     """sf_gdn_gated_norm_bwd on torch tensors.  Returns (dx, dgate, dw), with
     None for dgate without gate and for dw without w (or want_dw False).
     ``grads`` may supply preallocated outputs in that order."""
-    full = x.shape
-    x = _heads(x)
-    gate = _gate_rows(gate, full)
-    fields = _gated_norm_fields(x, gate, eps, scale, act)
-    dev, D = x.device, x.shape[2]
-    if w is not None:
-        _need(w, "w", torch.float32, (D,), dev)
-    _need(dy, "dy", x.dtype, full, dev)
-    want_dw = want_dw and w is not None
-    if grads is None:
-        grads = (torch.empty(full, dtype=x.dtype, device=dev),
-                 None if gate is None else torch.empty(full, dtype=x.dtype, device=dev),
-                 torch.empty(D, dtype=torch.float32, device=dev) if want_dw else None)
-        used_on(stream, *grads)
-    dx, dgate, dw = grads
-    _need(dx, "dx", x.dtype, full, dev)
-    if gate is not None:
-        _need(dgate, "dgate", x.dtype, full, dev)
-    elif dgate is not None:
-        raise ValueError("dgate without gate")
-    if want_dw:
-        _need(dw, "dw", torch.float32, (D,), dev)
-        workspace = _norm_workspace(gated_norm_bwd_workspace_bytes, GatedNormShape, fields,
-                                    workspace, dev, stream)
-    else:
-        dw = workspace = None
-    _run("sf_gdn_gated_norm_bwd", dev, stream, _shape_ref(GatedNormShape, *fields), x.data_ptr(),
-         _addr(gate), _addr(w), dy.data_ptr(), dx.data_ptr(), _addr(dgate), _addr(dw),
-         _addr(workspace), 0 if workspace is None else workspace.numel())
-    return dx, dgate, dw
-
-
-def _residual_norm_fields(x, eps, scale):
-    """ResidualNormShape's fields for x [..., C]."""
-    C = x.shape[-1]
-    return (x.numel() // C if C else 0), C, _dtype_code(x, "x"), float(eps), float(scale)
+    got = (_calls or load_calls()).gated_norm_bwd(x, gate, w, dy, eps, scale, act, grads, want_dw,
+                                                  workspace, _raw_stream(x, stream))
+    if stream is not None:
+        used_on(stream, *got)
+    return got[:3]
 
 
 def residual_norm_bwd_workspace_bytes(shape):
@@ -748,30 +571,12 @@ def residual_norm_fwd(x, r=None, w=None, s=None, scale=1.0, eps=1e-6, h=None, y=
     y = w * h / sqrt(mean(h^2) + eps) over the last dimension of x [..., C],
     with r like x (None: h is x), s [C] fp32 (None: ones) and w [C] fp32
     (None: ones).  Returns (y, h)."""
-    dev = _device_of(x, "x")
-    shape = _shape_ref(ResidualNormShape, *_residual_norm_fields(x, eps, scale))
-    full = x.shape
-    _need(x, "x", x.dtype, full, dev)
-    vec = full[-1:]
-    if w is not None:
-        _need(w, "w", torch.float32, vec, dev)
-    if s is not None:
-        _need(s, "s", torch.float32, vec, dev)
-    if r is not None:
-        _need(r, "r", x.dtype, full, dev)
-        if h is None:
-            h = _new(x, full, stream)
-        else:
-            _need(h, "h", x.dtype, full, dev)
-    elif s is not None or h is not None:
-        raise ValueError("s and h need r")
-    if y is None:
-        y = _new(x, full, stream)
-    else:
-        _need(y, "y", x.dtype, full, dev)
-    _run("sf_gdn_residual_norm_fwd", dev, stream, shape, x.data_ptr(), _addr(r), _addr(s),
-         _addr(w), _addr(h), y.data_ptr())
-    return y, (x if r is None else h)
+    got = (_calls or load_calls()).residual_norm_fwd(x, r, w, s, scale, eps, h, y,
+                                                     _raw_stream(x, stream))
+    if stream is not None:
+        used_on(stream, None if y is not None else got[0],
+                None if h is not None or r is None else got[1])
+    return got
 
 
 def residual_norm_bwd(h, r, w, s, dy, dh=None, scale=1.0, eps=1e-6, grads=None, want_dr=True,
@@ -781,43 +586,12 @@ def residual_norm_bwd(h, r, w, s, dy, dh=None, scale=1.0, eps=1e-6, grads=None, 
     ds): dr is None with want_dr False, dw without w, ds without s (r is read
     for ds only and may be None otherwise); ``grads`` may supply preallocated
     outputs in that order."""
-    dev = _device_of(h, "h")
-    fields = _residual_norm_fields(h, eps, scale)
-    C = h.shape[-1]
-    _need(h, "h", h.dtype, h.shape, dev)
-    _need(dy, "dy", h.dtype, h.shape, dev)
-    if dh is not None:
-        _need(dh, "dh", h.dtype, h.shape, dev)
-    for t, n in ((w, "w"), (s, "s")):
-        if t is not None:
-            _need(t, n, torch.float32, (C,), dev)
-    want_dw = want_dw and w is not None
-    want_ds = want_ds and s is not None
-    if want_ds:
-        _need(r, "r", h.dtype, h.shape, dev)
-    if grads is None:
-        grads = (torch.empty_like(h), torch.empty_like(h) if want_dr else None,
-                 torch.empty(C, dtype=torch.float32, device=dev) if want_dw else None,
-                 torch.empty(C, dtype=torch.float32, device=dev) if want_ds else None)
-        used_on(stream, *grads)
-    dx, dr, dw, ds = grads
-    _need(dx, "dx", h.dtype, h.shape, dev)
-    if want_dr:
-        _need(dr, "dr", h.dtype, h.shape, dev)
-    for t, n, want in ((dw, "dw", want_dw), (ds, "ds", want_ds)):
-        if want:
-            _need(t, n, torch.float32, (C,), dev)
-    if want_dw or want_ds:
-        workspace = _norm_workspace(residual_norm_bwd_workspace_bytes, ResidualNormShape, fields,
-                                    workspace, dev, stream)
-    else:
-        workspace = None
-    _run("sf_gdn_residual_norm_bwd", dev, stream, _shape_ref(ResidualNormShape, *fields),
-         h.data_ptr(), r.data_ptr() if want_ds else None, _addr(s), _addr(w), dy.data_ptr(),
-         _addr(dh), dx.data_ptr(), dr.data_ptr() if want_dr else None, dw.data_ptr() if want_dw else None,
-         ds.data_ptr() if want_ds else None, _addr(workspace),
-         0 if workspace is None else workspace.numel())
-    return dx, (dr if want_dr else None), (dw if want_dw else None), (ds if want_ds else None)
+    got = (_calls or load_calls()).residual_norm_bwd(h, r, w, s, dy, dh, scale, eps, grads, want_dr,
+                                                     want_dw, want_ds, workspace,
+                                                     _raw_stream(h, stream))
+    if stream is not None:
+        used_on(stream, *got)
+    return got[:4]
 
 
 class profile:

@@ -1,4 +1,5 @@
-"""Build libsf_gdn.so (HIP, gfx950) in the package directory.
+"""Build libsf_gdn.so (HIP, gfx950) and _calls.so (the native Python calls of
+the layer's operators) in the package directory.
 
     python -m linear_recurrence_chunked_gated_amd.build
 
@@ -8,6 +9,7 @@ then linked.  Packed-fp32 instruction forms are disabled for device code.
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -15,6 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsf_gdn.so")
 SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_conv.hip", "sf_gdn_api.cpp"]
+CALLS = os.path.join(HERE, "_calls.so")
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -35,14 +38,38 @@ def _compile(src):
     return obj, msgs
 
 
+def _build_calls():
+    """The CPython module _calls: host code on torch's headers, by g++."""
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = CALLS + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+           "-I", sysconfig.get_paths()["include"]]
+    for d in cpp_extension.include_paths():
+        cmd += ["-isystem", d]
+    cmd += [os.path.join(CSRC, "sf_gdn_calls.cpp"), "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu",
+            "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compile failed: %s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
+    os.replace(tmp, CALLS)
+    return r.stdout + r.stderr
+
+
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        calls = ex.submit(_build_calls)
         results = list(ex.map(_compile, SOURCES))
+        results_calls = calls.result()
     if verbose:
         for _, m in results:
             if m.strip():
                 print(m)
+        if results_calls.strip():
+            print(results_calls)
     tmp = LIB + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + [o for o, _ in results]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -380,6 +380,12 @@ def test_binding_refusals():
             (ValueError, lambda: gdn.gated_norm_fwd(x, None, w[:32])),
             (ValueError, lambda: gdn.gated_norm_fwd(x.view(2, 2, 2, 64), x)),
             (ValueError, lambda: gdn.gated_norm_fwd(x.view(2, 2, 2, 64).transpose(0, 1))),
+            (ValueError, lambda: gdn.gated_norm_fwd(x.view(2, 2, 2, 64)[:, :1].expand(2, 2, 2, 64))),
+            (ValueError, lambda: gdn.gated_norm_fwd(x[:1].expand(4, 2, 64))),
+            (TypeError, lambda: gdn.gated_norm_fwd(x, 3.0)),
+            (TypeError, lambda: gdn.gated_norm_bwd(x, None, w, x, grads=(x, None))),
+            (ValueError, lambda: gdn.gated_norm_bwd(x, None, w, x, grads=(None, None, None))),
+            (ValueError, lambda: gdn.gated_norm_bwd(x, None, w, x, workspace=torch.empty(1 << 20))),
             (ValueError, lambda: gdn.gated_norm_fwd(x.transpose(0, 1))),
             (ValueError, lambda: gdn.gated_norm_fwd(w)),
             (ValueError, lambda: gdn.gated_norm_bwd(x, None, w, x[:, :1])),
