@@ -67,7 +67,8 @@ __device__ __forceinline__ bool slot_repeats(const PoolBatch& b, int i, int slot
 // lanes and for a token that came alone or among others, so that a sequence's
 // outputs do not depend on how it was batched: columns go in units of four,
 // unit c of a row is summed with unit c + 16 (where D has it), that with unit
-// c + 8's sum, and the eight results in a tree.
+// c + 8's sum, and the eight results in a tree.  Which products are fused with
+// an addition is written out, for the same reason.
 //
 // x: this lane's part, on 16 lanes the sum of units l and l + 16, on 8 lanes
 // already joined with units l + 8 and l + 24; every lane gets the total.
@@ -79,20 +80,25 @@ __device__ __forceinline__ float sum_row_lanes(float x) {
   x += dpp_f<0x141>(x);
   return x;
 }
-__device__ __forceinline__ float add4(f32x4 x) { return (x[0] + x[1]) + (x[2] + x[3]); }
-// S . k over the row, in every lane
+// S . k over the row, in every lane (NE is H or 2 H)
 template <int NE, int L>
 __device__ __forceinline__ float row_dot(const f32x4 (&S)[NE], const f32x4 (&k)[NE]) {
-  constexpr int H = L == 8 ? 2 : 1;  // separate sums in a lane
-  f32x4 s[H];
+  constexpr int H = L == 8 ? 2 : 1;  // units summed apart in a lane
+  float x[H];
 #pragma unroll
-  for (int j = 0; j < NE; ++j)
+  for (int h = 0; h < H; ++h) {
+    if (NE == H) {
+      x[h] = __builtin_fmaf(S[h][0], k[h][0], S[h][1] * k[h][1]) +
+             __builtin_fmaf(S[h][2], k[h][2], S[h][3] * k[h][3]);
+    } else {
+      float s[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      s[j % H][i] = j < H ? S[j][i] * k[j][i] : __builtin_fmaf(S[j][i], k[j][i], s[j % H][i]);
-  float x = add4(s[0]);
-  if (H == 2) x += add4(s[1]);
-  return sum_row_lanes<L>(x);
+      for (int i = 0; i < 4; ++i)
+        s[i] = __builtin_fmaf(S[h + H][i], k[h + H][i], S[h][i] * k[h][i]);
+      x[h] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+  }
+  return sum_row_lanes<L>(H == 2 ? x[0] + x[H - 1] : x[0]);
 }
 // one unit of k . q
 __device__ __forceinline__ float unit_dot(f32x4 k, f32x4 q) {
@@ -101,9 +107,10 @@ __device__ __forceinline__ float unit_dot(f32x4 k, f32x4 q) {
 }
 
 constexpr int STEP_THREADS = 256;
-// Tokens staged in LDS at a time: two buffers stay under 20 KB, so that eight
-// workgroups share a compute unit.
-constexpr int STEP_TOKENS = 8;
+// Threads that stage a token, and tokens staged in LDS at a time (8 or 16): two
+// buffers take about 20 KB, so that seven workgroups share a compute unit.
+constexpr int step_token_threads(int D) { return D / 4; }
+constexpr int step_tokens(int D) { return STEP_THREADS / step_token_threads(D); }
 
 // Workgroup: 4 waves, each of 64 / L rows of one (sequence, value head)'s
 // state, a row on L lanes.  SINGLE: one token per sequence, straight from
@@ -188,30 +195,27 @@ __global__ __launch_bounds__(STEP_THREADS) void recurrent_step_kernel(StepArgs a
     x.g[2] = sum_row_lanes<L>(kq[0]);
     token(o + t * os, x);
   } else {
-    // Staging: 32 threads per token, each with a unit of four columns of k
-    // and q (half of the threads at D = 64) and the token's rows of v spread
-    // over them.
-    constexpr int TB = STEP_TOKENS;
-    constexpr int VV = (ROWS + 31) / 32;
-    static_assert(TB * 32 == STEP_THREADS, "one token per 32 threads");
+    // Staging: each thread of a token has a unit of four columns of k and q,
+    // and the token's rows of v are spread over them.
+    constexpr int TT = step_token_threads(D), TB = step_tokens(D);
+    constexpr int VV = (ROWS + TT - 1) / TT;
     typedef T vec4 __attribute__((ext_vector_type(4)));
     struct Chunk {
       f32x4 k[TB][D / 4], q[TB][D / 4];
-      float v[TB][VV * 32];
+      float v[TB][VV * TT];
       f32x4 g[TB];  // alpha, beta, k . q
     };
     __shared__ Chunk lds[2];
-    const int st = threadIdx.x / 32, sl = threadIdx.x % 32;  // token of the chunk, thread in it
-    const int su = sl % (D / 4);                             // its unit
+    const int st = threadIdx.x / TT, sl = threadIdx.x % TT;  // token of the chunk, unit in it
     vec4 rk, rq;
     T rv[VV];
     float ra = 0.f, rb = 0.f;
     auto load = [&](int c) {
       const size_t t = min(c + st, e.t1 - 1);  // past the end: the last token again, not used
-      rk = *reinterpret_cast<const vec4*>(k + t * a.ks + su * 4);
-      rq = *reinterpret_cast<const vec4*>(q + t * a.qs + su * 4);
+      rk = *reinterpret_cast<const vec4*>(k + t * a.ks + sl * 4);
+      rq = *reinterpret_cast<const vec4*>(q + t * a.qs + sl * 4);
 #pragma unroll
-      for (int i = 0; i < VV; ++i) rv[i] = v[t * a.vs + min(i * 32 + sl, ROWS - 1)];
+      for (int i = 0; i < VV; ++i) rv[i] = v[t * a.vs + min(i * TT + sl, ROWS - 1)];
       ra = a.alpha[t * a.Hv + hv];
       rb = a.beta[t * a.Hv + hv];
     };
@@ -220,12 +224,10 @@ __global__ __launch_bounds__(STEP_THREADS) void recurrent_step_kernel(StepArgs a
       float kq = unit_dot(kf, qf);
       if (D == 128) kq += __shfl_xor(kq, 16);
       kq = sum_row_lanes<16>(kq);
-      if (sl < D / 4) {
-        b.k[st][su] = kf;
-        b.q[st][su] = qf;
-      }
+      b.k[st][sl] = kf;
+      b.q[st][sl] = qf;
 #pragma unroll
-      for (int i = 0; i < VV; ++i) b.v[st][i * 32 + sl] = (float)rv[i];
+      for (int i = 0; i < VV; ++i) b.v[st][i * TT + sl] = (float)rv[i];
       if (sl == 0) b.g[st] = f32x4{ra, rb, kq, 0.f};
     };
     load(e.t0);
