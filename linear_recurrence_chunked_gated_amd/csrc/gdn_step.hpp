@@ -17,7 +17,7 @@
 // value heads at D = 128 (1.08 GB) take 182 us, 5.9 TB/s; a plain device copy
 // of 1 GiB runs at 5.1 TB/s.  64 sequences of 1 to 8 tokens and 16 heads (139
 // MB) take 27 us, 5.1 TB/s.  A long run is bound by a token's dependent
-// arithmetic, 0.25 us: one sequence of 256 tokens takes 65 us.
+// arithmetic, 0.24 us: one sequence of 256 tokens takes 62 us.
 #pragma once
 #include "gdn_kernels.hpp"
 
@@ -161,15 +161,15 @@ __global__ __launch_bounds__(STEP_THREADS) void recurrent_step_kernel(StepArgs a
     f32x4 g;  // alpha, beta, k . q
     float v;
   };
-  auto token = [&](T* ot, const Token& x) {
+  auto token = [&](const Token& x) {
     const float p = row_dot<NE, L>(S, x.k), s = row_dot<NE, L>(S, x.q);
     const float u = x.g[1] * __builtin_fmaf(-x.g[0], p, x.v);
     const float y = __builtin_fmaf(u, x.g[2], x.g[0] * s);
-    if (l == 0) *ot = (T)y;
 #pragma unroll
     for (int j = 0; j < NE; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) S[j][i] = __builtin_fmaf(u, x.k[j][i], x.g[0] * S[j][i]);
+    return y;
   };
 
   if constexpr (SINGLE) {
@@ -193,7 +193,8 @@ __global__ __launch_bounds__(STEP_THREADS) void recurrent_step_kernel(StepArgs a
     x.g[0] = a.alpha[t * a.Hv + hv];
     x.g[1] = a.beta[t * a.Hv + hv];
     x.g[2] = sum_row_lanes<L>(kq[0]);
-    token(o + t * os, x);
+    const float y = token(x);
+    if (l == 0) o[t * os] = (T)y;
   } else {
     // Staging: each thread of a token has a unit of four columns of k and q,
     // and the token's rows of v are spread over them.
@@ -230,8 +231,8 @@ __global__ __launch_bounds__(STEP_THREADS) void recurrent_step_kernel(StepArgs a
       for (int i = 0; i < VV; ++i) b.v[st][i * TT + sl] = (float)rv[i];
       if (sl == 0) b.g[st] = f32x4{ra, rb, kq, 0.f};
     };
-    load(e.t0);
     T* ot = o + e.t0 * os;
+    load(e.t0);
 #pragma unroll 1
     for (int c = e.t0, buf = 0; c < e.t1; c += TB, buf ^= 1) {
       // this buffer's readers (two chunks back) have passed the last barrier
@@ -250,21 +251,41 @@ __global__ __launch_bounds__(STEP_THREADS) void recurrent_step_kernel(StepArgs a
         x.v = b.v[i][wrow];
       };
       Token x;
-      if (L == 16) {
-        // few workgroups, few waves to hide the LDS reads: a token ahead
-        read(0, x);
-#pragma unroll 1
-        for (int i = 0; i < m; ++i, ot += os) {
+      if constexpr (L == 16) {
+        // Few workgroups, a wave or two per SIMD: what counts is a token's own
+        // latency.  The next token is read from LDS ahead, four tokens run
+        // without a branch between them, and lane i keeps token i's output to
+        // store it after the chunk (33 tokens of a 64-wide fp32 state: 7.7 us
+        // instead of 8.8).  With many workgroups the late stores cost more
+        // than the branches (64 sequences of 4 tokens in fp32: 54 us instead
+        // of 51).
+        static_assert(TB <= L, "a lane for each token's output");
+        constexpr int U = 4;
+        float out = 0.f;
+        auto step = [&](int i) {
           Token y;
           read(min(i + 1, m - 1), y);
-          token(ot, x);
+          const float r = token(x);
+          out = l == i ? r : out;
           x = y;
+        };
+        read(0, x);
+        int i = 0;
+#pragma unroll 1
+        for (; i + U <= m; i += U) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) step(i + u);
         }
+#pragma unroll 1
+        for (; i < m; ++i) step(i);
+        if (l < m) ot[l * os] = (T)out;
+        ot += m * os;
       } else {
 #pragma unroll 1
         for (int i = 0; i < m; ++i, ot += os) {
           read(i, x);
-          token(ot, x);
+          const float y = token(x);
+          if (l == 0) *ot = (T)y;
         }
       }
     }
@@ -298,7 +319,7 @@ static hipError_t step_launch(const StepArgs& a, hipStream_t st, Profiler* prof)
 //    instead of 36.2 for 96 MiB and 19.9 instead of 17.3 for 48 MiB;
 //  - with several tokens and too few workgroups of eight-lane rows to give
 //    every compute unit one, 16 lanes a row halve each token's arithmetic:
-//    one sequence of 256 tokens 65 us instead of 83, two of 8 tokens 4.5
+//    one sequence of 256 tokens 62 us instead of 83, two of 8 tokens 4.5
 //    instead of 5.1; at 256 workgroups both take 5.4 and beyond, the eight
 //    lanes are faster (8 sequences of 8 tokens 7.5 instead of 8.6).
 template <typename T, int D>
