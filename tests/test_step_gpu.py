@@ -171,6 +171,35 @@ def test_two_calls_at_once():
         assert torch.equal(g, w)
 
 
+def test_threads_on_streams_of_their_own():
+    """Two host threads, each decoding 20 steps on its own stream and pool."""
+    import threading
+    batches = [_cuda(step_inputs([1] * n, 2, 2, 64, "bf16", n, seed=95 + n)) for n in (9, 33)]
+
+    def decode(c, stream, out):
+        with torch.cuda.stream(stream):
+            s = c["state"].clone()
+            for _ in range(20):
+                o = gdn.recurrent_step(c["q"], c["k"], c["v"], c["alpha"], c["beta"], s, c["slots"])
+                gdn.gated_norm_fwd(o, o)
+            out.append((o, s))
+
+    want, got = [], [[], []]
+    for c in batches:
+        decode(c, torch.cuda.current_stream(), want)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    threads = [threading.Thread(target=decode, args=(c, st, out))
+               for c, st, out in zip(batches, streams, got)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for (o, s), ((ro, rs),) in zip(want, got):
+        assert torch.equal(o, ro) and torch.equal(s, rs)
+
+
 def test_step_strided_rows():
     """q, k and v as slices of one projection's rows."""
     lens = [2, 7, 1]
