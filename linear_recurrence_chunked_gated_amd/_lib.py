@@ -480,16 +480,39 @@ def load_calls():
     return _calls
 
 
-def _raw_stream(t, stream):
-    """The stream handle for a call on t's device: the current stream there
-    when None."""
-    if stream is None and t.is_cuda:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+def _raw_stream(t):
+    """The handle of the current stream on t's device."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a GPU device, got one on %s" % t.device)
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _none(got):  # no output was made
+    return ()
+
+
+def _call_on(stream, t, f, *args, made=None):
+    """f(*args, handle) of the native module for work on ``stream``.
+
+    What f allocates comes from the current stream's memory, and a block of
+    that may have been freed with work of the current stream on it still
+    pending, which ``stream`` does not wait for; so ``stream`` is made the
+    current one for the call.  The outputs made here (made(result); None: all
+    of them) are marked as used by the caller's current stream, where they may
+    then be read and freed as well (after it has waited for ``stream``)."""
     if not t.is_cuda:
         raise ValueError("tensors must be on a GPU device, got one on %s" % t.device)
     if stream.device != t.device:
         raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
-    return stream.cuda_stream
+    here = torch.cuda.current_stream(stream.device)
+    if stream == here:
+        return f(*args, stream.cuda_stream)
+    with torch.cuda.stream(stream):
+        got = f(*args, stream.cuda_stream)
+    for m in (got if isinstance(got, tuple) else (got,)) if made is None else made(got):
+        if m is not None and m.numel() > 0:
+            m.record_stream(here)
+    return got
 
 
 def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=None, update=True,
@@ -503,12 +526,16 @@ def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=No
     int32 names each sequence's slot (None: sequence i has slot i, one for
     every slot; negative: padding), seq_start [n_seq + 1] int32 its token rows
     (None: n_tok / n_seq each).  Returns o [n_tok, Hv, Dv]; rows of padding
-    and past the last sequence keep what o held (pass o to set it)."""
-    got = (_calls or load_calls()).recurrent_step(q, k, v, alpha, beta, state, slots, seq_start, o,
-                                                  update, _raw_stream(q, stream))
-    if stream is not None and o is None:
-        used_on(stream, got)
-    return got
+    and past the last sequence keep what o held (pass o to set it).
+
+    With ``stream``, here and in the calls below, the kernels run there, in no
+    order with the current stream's work but what the caller sets up; outputs
+    that the call makes are the given stream's memory."""
+    f = (_calls or load_calls()).recurrent_step
+    args = q, k, v, alpha, beta, state, slots, seq_start, o, update
+    if stream is None:
+        return f(*args, _raw_stream(q))
+    return _call_on(stream, q, f, *args, made=None if o is None else _none)
 
 
 def shortconv_step(x, w, state, slots=None, seq_start=None, act=0, y=None, update=True,
@@ -519,11 +546,11 @@ def shortconv_step(x, w, state, slots=None, seq_start=None, act=0, y=None, updat
     x [n_tok, C] (token rows may be slices of wider rows), w [C, W] fp32,
     state [n_slots, W-1, C] in x's dtype, advanced in place unless update is
     False; slots and seq_start as in recurrent_step.  Returns y [n_tok, C]."""
-    got = (_calls or load_calls()).shortconv_step(x, w, state, slots, seq_start, act, y, update,
-                                                  _raw_stream(x, stream))
-    if stream is not None and y is None:
-        used_on(stream, got)
-    return got
+    f = (_calls or load_calls()).shortconv_step
+    args = x, w, state, slots, seq_start, act, y, update
+    if stream is None:
+        return f(*args, _raw_stream(x))
+    return _call_on(stream, x, f, *args, made=None if y is None else _none)
 
 
 def gated_norm_bwd_workspace_bytes(shape):
@@ -539,11 +566,11 @@ def gated_norm_fwd(x, gate=None, w=None, eps=1e-6, scale=1.0, act=1, y=None, str
     gate like x or None (factor 1) and w [D] fp32 or None (ones); act 1 for
     SiLU, 0 for the gate itself.  x and gate may be head slices of wider token
     rows."""
-    got = (_calls or load_calls()).gated_norm_fwd(x, gate, w, eps, scale, act, y,
-                                                  _raw_stream(x, stream))
-    if stream is not None and y is None:
-        used_on(stream, got)
-    return got
+    f = (_calls or load_calls()).gated_norm_fwd
+    args = x, gate, w, eps, scale, act, y
+    if stream is None:
+        return f(*args, _raw_stream(x))
+    return _call_on(stream, x, f, *args, made=None if y is None else _none)
 
 
 def gated_norm_bwd(x, gate, w, dy, eps=1e-6, scale=1.0, act=1, grads=None, want_dw=True,
@@ -551,11 +578,12 @@ def gated_norm_bwd(x, gate, w, dy, eps=1e-6, scale=1.0, act=1, grads=None, want_
     """sf_gdn_gated_norm_bwd on torch tensors.  Returns (dx, dgate, dw), with
     None for dgate without gate and for dw without w (or want_dw False).
     ``grads`` may supply preallocated outputs in that order."""
-    got = (_calls or load_calls()).gated_norm_bwd(x, gate, w, dy, eps, scale, act, grads, want_dw,
-                                                  workspace, _raw_stream(x, stream))
-    if stream is not None:
-        used_on(stream, *got)
-    return got[:3]
+    f = (_calls or load_calls()).gated_norm_bwd
+    args = x, gate, w, dy, eps, scale, act, grads, want_dw, workspace
+    if stream is None:
+        return f(*args, _raw_stream(x))[:3]
+    return _call_on(stream, x, f, *args,
+                    made=lambda got: got[:3] if grads is None else ())[:3]
 
 
 def residual_norm_bwd_workspace_bytes(shape):
@@ -571,12 +599,13 @@ def residual_norm_fwd(x, r=None, w=None, s=None, scale=1.0, eps=1e-6, h=None, y=
     y = w * h / sqrt(mean(h^2) + eps) over the last dimension of x [..., C],
     with r like x (None: h is x), s [C] fp32 (None: ones) and w [C] fp32
     (None: ones).  Returns (y, h)."""
-    got = (_calls or load_calls()).residual_norm_fwd(x, r, w, s, scale, eps, h, y,
-                                                     _raw_stream(x, stream))
-    if stream is not None:
-        used_on(stream, None if y is not None else got[0],
-                None if h is not None or r is None else got[1])
-    return got
+    f = (_calls or load_calls()).residual_norm_fwd
+    args = x, r, w, s, scale, eps, h, y
+    if stream is None:
+        return f(*args, _raw_stream(x))
+    return _call_on(stream, x, f, *args,
+                    made=lambda got: (None if y is not None else got[0],
+                                      None if h is not None or r is None else got[1]))
 
 
 def residual_norm_bwd(h, r, w, s, dy, dh=None, scale=1.0, eps=1e-6, grads=None, want_dr=True,
@@ -586,12 +615,12 @@ def residual_norm_bwd(h, r, w, s, dy, dh=None, scale=1.0, eps=1e-6, grads=None, 
     ds): dr is None with want_dr False, dw without w, ds without s (r is read
     for ds only and may be None otherwise); ``grads`` may supply preallocated
     outputs in that order."""
-    got = (_calls or load_calls()).residual_norm_bwd(h, r, w, s, dy, dh, scale, eps, grads, want_dr,
-                                                     want_dw, want_ds, workspace,
-                                                     _raw_stream(h, stream))
-    if stream is not None:
-        used_on(stream, *got)
-    return got[:4]
+    f = (_calls or load_calls()).residual_norm_bwd
+    args = h, r, w, s, dy, dh, scale, eps, grads, want_dr, want_dw, want_ds, workspace
+    if stream is None:
+        return f(*args, _raw_stream(h))[:4]
+    return _call_on(stream, h, f, *args,
+                    made=lambda got: got[:4] if grads is None else ())[:4]
 
 
 class profile:
