@@ -155,15 +155,36 @@ def _stream(stream):
 
 
 def used_on(stream, *tensors):
-    """Mark tensors that this module allocated on the current stream as in
-    use by ``stream`` when the kernels run there, so that the caching
-    allocator does not hand their memory to current-stream work before the
-    kernels are done (tensor.record_stream).  No-op for the current stream."""
+    """Mark tensors that this package allocated on the current stream as in
+    use by ``stream`` when kernels run there as well, so that the caching
+    allocator does not hand their memory to current-stream work before those
+    are done (tensor.record_stream).  No-op for the current stream."""
     if stream is None or stream == torch.cuda.current_stream(stream.device):
         return
     for t in tensors:
         if t is not None and t.numel() > 0:
             t.record_stream(stream)
+
+
+def new_on(stream, make, *args, **kw):
+    """make(*args, **kw), a new tensor (or None), for kernels on ``stream``
+    (None: the current one).
+
+    A block of the current stream's memory may have been freed with work of
+    that stream on it still pending, which ``stream`` does not wait for, so the
+    tensor is made with ``stream`` the current one (a fill then runs there
+    too), and marked as used by the caller's current stream, where it may be
+    read and freed as well."""
+    if stream is None:
+        return make(*args, **kw)
+    here = torch.cuda.current_stream(stream.device)
+    if stream == here:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        t = make(*args, **kw)
+    if t is not None and t.numel() > 0:
+        t.record_stream(here)
+    return t
 
 
 def make_shape(B, T, H, Dk, Dv, dtype, seg_blocks=0):
@@ -239,24 +260,20 @@ def chunk_fwd(q, k, v, alpha, beta, S_in=None, o=None, S_out=None, seg_blocks=0,
     if S_in is not None:
         _need(S_in, "S_in", torch.float32, (B, H, Dv, Dk), dev)
     if o is None:
-        o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
-        used_on(stream, o)
+        o = new_on(stream, torch.empty, (B, T, H, Dv), dtype=q.dtype, device=dev)
     _need(o, "o", q.dtype, (B, T, H, Dv), dev)
     if S_out is None:
-        S_out = torch.empty((B, H, Dv, Dk), dtype=torch.float32, device=dev)
-        used_on(stream, S_out)
+        S_out = new_on(stream, torch.empty, (B, H, Dv, Dk), dtype=torch.float32, device=dev)
     _need(S_out, "S_out", torch.float32, (B, H, Dv, Dk), dev)
     shape = make_shape(B, T, H, Dk, Dv, q.dtype, seg_blocks)
     need = workspace_bytes(shape)
     if workspace is None or workspace.numel() < need:
-        workspace = alloc_workspace(need, dev)
-        used_on(stream, workspace)
+        workspace = new_on(stream, alloc_workspace, need, dev)
     wsn = ctypes.c_size_t(0 if workspace is None else workspace.numel())
     if saved is True:
         n = saved_bytes(shape)
-        saved = (alloc_workspace(n, dev) if n else
+        saved = (new_on(stream, alloc_workspace, n, dev) if n else
                  torch.empty(0, dtype=torch.uint8, device=dev))
-        used_on(stream, saved)
     if phase != PHASE_ALL:
         st = load().sf_gdn_chunk_fwd_split(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
                                            _ptr(alpha), _ptr(beta), _ptr(S_in), _ptr(o),
@@ -297,12 +314,10 @@ def chunk_fwd_noalloc(q, k, v, alpha, beta, S_in=None, o=None, S_out=None, seg_b
     if S_in is not None:
         _need(S_in, "S_in", torch.float32, (B, H, Dv, Dk), dev)
     if o is None:
-        o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=dev)
-        used_on(stream, o)
+        o = new_on(stream, torch.empty, (B, T, H, Dv), dtype=q.dtype, device=dev)
     _need(o, "o", q.dtype, (B, T, H, Dv), dev)
     if S_out is None:
-        S_out = torch.empty((B, H, Dv, Dk), dtype=torch.float32, device=dev)
-        used_on(stream, S_out)
+        S_out = new_on(stream, torch.empty, (B, H, Dv, Dk), dtype=torch.float32, device=dev)
     _need(S_out, "S_out", torch.float32, (B, H, Dv, Dk), dev)
     shape = make_shape(B, T, H, Dk, Dv, q.dtype, seg_blocks)
     st = load().sf_gdn_chunk_fwd_noalloc(ctypes.byref(shape), _ptr(q), _ptr(k), _ptr(v),
@@ -336,16 +351,13 @@ def chunk_bwd(q, k, v, alpha, beta, S_in, dO, dS_out=None, grads=None, seg_block
     if dS_out is not None:
         _need(dS_out, "dS_out", torch.float32, (B, H, Dv, Dk), dev)
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
-                 torch.empty_like(alpha), torch.empty_like(beta),
-                 torch.empty((B, H, Dv, Dk), dtype=torch.float32, device=dev))
-        used_on(stream, *grads)
+        grads = [new_on(stream, torch.empty_like, t) for t in (q, k, v, alpha, beta)]
+        grads.append(new_on(stream, torch.empty, (B, H, Dv, Dk), dtype=torch.float32, device=dev))
     dq, dk, dv, da, db, dS_in = grads
     shape = make_shape(B, T, H, Dk, Dv, q.dtype, seg_blocks)
     need = workspace_bytes(shape, backward=True)
     if workspace is None or workspace.numel() < need:
-        workspace = alloc_workspace(need, dev)
-        used_on(stream, workspace)
+        workspace = new_on(stream, alloc_workspace, need, dev)
     wsn = ctypes.c_size_t(0 if workspace is None else workspace.numel())
     if phase != PHASE_ALL:
         if saved is None:
@@ -401,12 +413,10 @@ def shortconv_fwd(x, w, conv_in=None, act=0, y=None, conv_out=None, want_state=T
     if conv_in is not None:
         _need(conv_in, "conv_in", x.dtype, (B, W - 1, C), dev)
     if y is None:
-        y = torch.empty_like(x)
-        used_on(stream, y)
+        y = new_on(stream, torch.empty_like, x)
     _need(y, "y", x.dtype, (B, T, C), dev)
     if want_state and conv_out is None and W > 1:
-        conv_out = torch.empty((B, W - 1, C), dtype=x.dtype, device=dev)
-        used_on(stream, conv_out)
+        conv_out = new_on(stream, torch.empty, (B, W - 1, C), dtype=x.dtype, device=dev)
     shape = conv_shape(B, T, C, W, x.dtype, act)
     _check(load().sf_gdn_shortconv_fwd(ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(conv_in),
                                        _ptr(y), _ptr(conv_out) if W > 1 else None,
@@ -429,19 +439,15 @@ def shortconv_bwd(x, w, conv_in, dy, dconv_out=None, act=0, dx=None, dw=None, wa
         if t is not None:
             _need(t, n, x.dtype, (B, W - 1, C), dev)
     if dx is None:
-        dx = torch.empty_like(x)
-        used_on(stream, dx)
+        dx = new_on(stream, torch.empty_like, x)
     if dw is None:
-        dw = torch.empty_like(w)
-        used_on(stream, dw)
-    dci = (torch.empty((B, W - 1, C), dtype=x.dtype, device=dev)
+        dw = new_on(stream, torch.empty_like, w)
+    dci = (new_on(stream, torch.empty, (B, W - 1, C), dtype=x.dtype, device=dev)
            if want_state and W > 1 else None)
-    used_on(stream, dci)
     shape = conv_shape(B, T, C, W, x.dtype, act)
     need = shortconv_bwd_workspace_bytes(shape)
     if workspace is None or workspace.numel() < need:
-        workspace = alloc_workspace(need, dev)
-        used_on(stream, workspace)
+        workspace = new_on(stream, alloc_workspace, need, dev)
     _check(load().sf_gdn_shortconv_bwd(ctypes.byref(shape), _ptr(x), _ptr(w), _ptr(conv_in),
                                        _ptr(dy), _ptr(dconv_out), _ptr(dx), _ptr(dw), _ptr(dci),
                                        _ptr(workspace),

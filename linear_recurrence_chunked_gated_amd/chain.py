@@ -64,20 +64,20 @@ def _overlapped(n, begin, end, stream, side, order):
             ev_begin = side.record_event()
 
 
-def _ws_pair(workspaces, shapes, backward, dev, streams):
+def _ws_pair(workspaces, shapes, backward, dev, main, side):
     if workspaces is not None:
         return workspaces
     need = max(_lib.workspace_bytes(s, backward=backward) for s in shapes)
-    ws = [_lib.alloc_workspace(need, dev), _lib.alloc_workspace(need, dev)]
-    _used_on(streams, *ws)
-    return ws
+    return [_new(main, side, _lib.alloc_workspace, need, dev) for _ in range(2)]
 
 
-def _used_on(streams, *tensors):
-    """Buffers allocated here (on the current stream) that kernels on
-    ``streams`` use: see _lib.used_on."""
-    for st in streams:
-        _lib.used_on(st, *tensors)
+def _new(main, side, make, *args, **kw):
+    """A buffer for kernels on ``main`` (_lib.new_on) and, after those of main
+    so far, on ``side``."""
+    t = _lib.new_on(main, make, *args, **kw)
+    if t is not None:
+        _lib.used_on(side, t)
+    return t
 
 
 def chain_fwd(q, k, v, alpha, beta, S_in, lengths, o=None, seg_blocks=0, stream=None,
@@ -108,25 +108,22 @@ def chain_fwd(q, k, v, alpha, beta, S_in, lengths, o=None, seg_blocks=0, stream=
         lengths = split_lengths(lengths, split)
     bnd = _bounds(lengths, T)
     if o is None:
-        o = torch.empty((B, T, H, Dv), dtype=q.dtype, device=q.device)
-        _used_on([stream, side_stream], o)
+        o = _new(stream, side_stream, torch.empty, (B, T, H, Dv), dtype=q.dtype, device=q.device)
     if overlap:
         dev = q.device
         main = stream if stream is not None else torch.cuda.current_stream(dev)
         side = side_stream if side_stream is not None else torch.cuda.Stream(device=dev)
         shapes = [_lib.make_shape(B, n, H, Dk, Dv, q.dtype, seg_blocks) for n in lengths]
-        ws = _ws_pair(workspaces, shapes, False, dev, [main, side])
+        ws = _ws_pair(workspaces, shapes, False, dev, main, side)
         if save and saved is None:
-            saved = [_lib.alloc_workspace(_lib.saved_bytes(s), dev) for s in shapes]
-            _used_on([main, side], *saved)
+            saved = [_new(main, side, _lib.alloc_workspace, _lib.saved_bytes(s), dev)
+                     for s in shapes]
         if states is None:
             states = [S_in if S_in is not None else
-                      torch.zeros((B, H, Dv, Dk), dtype=torch.float32, device=dev)]
-            states += [torch.empty((B, H, Dv, Dk), dtype=torch.float32, device=dev)
-                       for _ in lengths]
-            _used_on([main, side], *states[1:])
-            if S_in is None:
-                _used_on([main, side], states[0])
+                      _new(main, side, torch.zeros, (B, H, Dv, Dk), dtype=torch.float32,
+                           device=dev)]
+            states += [_new(main, side, torch.empty, (B, H, Dv, Dk), dtype=torch.float32,
+                            device=dev) for _ in lengths]
         sv = saved if save else [None] * len(lengths)
 
         def call(i, slot, st, phase):
@@ -140,14 +137,13 @@ def chain_fwd(q, k, v, alpha, beta, S_in, lengths, o=None, seg_blocks=0, stream=
                     list(range(len(lengths))))
         return (o, states, saved) if save else (o, states)
     states = [S_in if S_in is not None else
-              torch.zeros((B, H, Dv, Dk), dtype=torch.float32, device=q.device)]
-    if S_in is None:
-        _used_on([stream], states[0])
+              _lib.new_on(stream, torch.zeros, (B, H, Dv, Dk), dtype=torch.float32,
+                          device=q.device)]
     saved = []
     for i in range(len(lengths)):
         sl = slice(bnd[i], bnd[i + 1])
-        S_next = torch.empty((B, H, Dv, Dk), dtype=torch.float32, device=q.device)
-        _used_on([stream], S_next)
+        S_next = _lib.new_on(stream, torch.empty, (B, H, Dv, Dk), dtype=torch.float32,
+                             device=q.device)
         r = _lib.chunk_fwd(q[:, sl], k[:, sl], v[:, sl], alpha[:, sl], beta[:, sl], states[i],
                            o=o[:, sl], S_out=S_next, seg_blocks=seg_blocks, stream=stream,
                            saved=True if save else None)
@@ -183,9 +179,7 @@ def chain_bwd(q, k, v, alpha, beta, dO, dS_out, lengths, states, grads=None, seg
         raise ValueError("%d saved buffers for %d chunks (was the forward split the same way?)"
                          % (len(saved), len(lengths)))
     if grads is None:
-        grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v),
-                 torch.empty_like(alpha), torch.empty_like(beta))
-        _used_on([stream, side_stream], *grads)
+        grads = [_new(stream, side_stream, torch.empty_like, t) for t in (q, k, v, alpha, beta)]
     dq, dk, dv, da, db = grads
     if overlap:
         if saved is None:
@@ -194,11 +188,10 @@ def chain_bwd(q, k, v, alpha, beta, dO, dS_out, lengths, states, grads=None, seg
         main = stream if stream is not None else torch.cuda.current_stream(dev)
         side = side_stream if side_stream is not None else torch.cuda.Stream(device=dev)
         shapes = [_lib.make_shape(B, n, H, Dk, Dv, q.dtype, seg_blocks) for n in lengths]
-        ws = _ws_pair(workspaces, shapes, True, dev, [main, side])
+        ws = _ws_pair(workspaces, shapes, True, dev, main, side)
         if state_grads is None:
-            state_grads = [torch.empty((B, H, Dv, Dk), dtype=torch.float32, device=dev)
-                           for _ in lengths]
-            _used_on([main, side], *state_grads)
+            state_grads = [_new(main, side, torch.empty, (B, H, Dv, Dk), dtype=torch.float32,
+                                device=dev) for _ in lengths]
         n = len(lengths)
 
         def call(i, slot, st, phase):
@@ -217,8 +210,8 @@ def chain_bwd(q, k, v, alpha, beta, dO, dS_out, lengths, states, grads=None, seg
     G = dS_out
     for i in range(len(lengths) - 1, -1, -1):
         sl = slice(bnd[i], bnd[i + 1])
-        G_prev = torch.empty((B, H, Dv, Dk), dtype=torch.float32, device=q.device)
-        _used_on([stream], G_prev)
+        G_prev = _lib.new_on(stream, torch.empty, (B, H, Dv, Dk), dtype=torch.float32,
+                             device=q.device)
         _lib.chunk_bwd(q[:, sl], k[:, sl], v[:, sl], alpha[:, sl], beta[:, sl],
                        None if saved is not None else states[i],
                        dO[:, sl], G, grads=(dq[:, sl], dk[:, sl], dv[:, sl], da[:, sl],

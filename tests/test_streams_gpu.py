@@ -49,8 +49,55 @@ def _residual_norm_bwd(stream):
     return lambda: gdn.residual_norm_bwd(h, r, w, w, dy, dh, stream=stream)
 
 
+def _chunk(T=200, H=4, D=64):
+    q, k = (torch.nn.functional.normalize(rnd(1, T, H, D, seed=i), dim=-1) for i in (1, 2))
+    return (q, k, rnd(1, T, H, D, seed=3), rnd(1, T, H, seed=4).sigmoid(),
+            rnd(1, T, H, seed=5).sigmoid())
+
+
+def _chunk_fwd(stream):
+    x = _chunk()
+    return lambda: gdn.chunk_fwd(*x, stream=stream, saved=True)[:2]
+
+
+def _chunk_bwd(stream):
+    x, dO, dS = _chunk(), rnd(1, 200, 4, 64, seed=6), rnd(1, 4, 64, 64, seed=7)
+    return lambda: gdn.chunk_bwd(*x, None, dO, dS, stream=stream)
+
+
+def _shortconv_fwd(stream):
+    x, w = rnd(2, 300, 512, seed=1), rnd(512, 4, seed=2)
+    return lambda: gdn.shortconv_fwd(x, w, stream=stream)
+
+
+def _shortconv_bwd(stream):
+    x, w, dy = rnd(2, 300, 512, seed=1), rnd(512, 4, seed=2), rnd(2, 300, 512, seed=3)
+    return lambda: gdn.shortconv_bwd(x, w, None, dy, stream=stream)
+
+
+def _chain(stream, overlap):
+    x, dO, dS = _chunk(), rnd(1, 200, 4, 64, seed=6), rnd(1, 4, 64, 64, seed=7)
+    lens = [64, 100, 36]
+
+    def call():
+        o, states, saved = gdn.chain_fwd(*x, None, lens, stream=stream, save=True, overlap=overlap)
+        grads = gdn.chain_bwd(*x, dO, dS, lens, states, stream=stream, saved=saved,
+                              overlap=overlap)
+        return (o, *states, *grads)
+    return call
+
+
+def _chain_plain(stream):
+    return _chain(stream, False)
+
+
+def _chain_overlapped(stream):
+    return _chain(stream, True)
+
+
 CALLS = [_recurrent_step, _shortconv_step, _gated_norm_fwd, _gated_norm_bwd, _residual_norm_fwd,
-         _residual_norm_bwd]
+         _residual_norm_bwd, _chunk_fwd, _chunk_bwd, _shortconv_fwd, _shortconv_bwd, _chain_plain,
+         _chain_overlapped]
 
 
 @pytest.mark.parametrize("make", CALLS, ids=lambda f: f.__name__.strip("_"))

@@ -104,3 +104,20 @@ def test_outputs_of_the_caller_are_not_marked(streams):
     made, here = Made(), streams.current
     gdn.residual_norm_fwd(X, stream=Stream())
     assert made.marked == [here] and all(t.marked == [] for t in mine)
+
+
+@pytest.mark.parametrize("given", ["none", "current", "side"])
+def test_new_buffers_belong_to_the_given_stream(streams, given):
+    """The chunk, convolution and chain calls make their buffers by new_on."""
+    here = streams.current
+    stream = {"none": None, "current": here, "side": Stream()}[given]
+
+    def make(n, dtype=None):
+        streams.calls.append(streams.current)
+        assert n == 3 and dtype == "x"
+        return Made()
+
+    t = _lib.new_on(stream, make, 3, dtype="x")
+    assert streams.calls == [stream if given == "side" else here] and streams.current is here
+    assert t.marked == ([here] if given == "side" else [])
+    assert _lib.new_on(stream, lambda: None) is None  # an empty workspace
