@@ -249,7 +249,9 @@ sf_status sf_gdn_shortconv_bwd(const sf_conv_shape* shape, const void* x, const 
  *   - rows of no sequence (past the last offset) keep their output's contents;
  *   - an entry whose slot is not below n_slots, or with update = 1 repeats the
  *     slot of an earlier entry, is refused: its output rows are NaN and no
- *     state is touched for it.  With update = 0 entries may share a slot;
+ *     state is touched for it.  With update = 0 entries may share a slot.
+ *     The look for repeats grows with the square of n_seq, so slots with
+ *     update = 1 go up to 65,536 sequences (SF_ERR_UNSUPPORTED beyond);
  *   - offsets are clamped to 0 .. n_tok; no entry reaches outside the tensors.
  * Token rows of q, k, v (x) may lie stride elements apart, e.g. as slices of
  * one projection's rows: 0 means contiguous, else a multiple of 8, at least

@@ -813,13 +813,21 @@ sf_status check_apart(const std::vector<Range>& in, const std::vector<Range>& ou
   return SF_OK;
 }
 
-// The pool batch of a step call; *stride of a token tensor: 0 means `width`.
-sf_status make_batch(int n_seq, int n_tok, int n_slots, const int* slots, const int* seq_start,
-                     PoolBatch& b) {
+// Every workgroup of an updating call looks for its slot among the earlier
+// entries, so that check grows with the square of their number.  At this limit
+// the step takes 16.2 ms with it and 5.7 without (16 heads, D = 64), 80 and 48
+// (32 heads, D = 128), the convolution 8.5 and 1.3 (6144 channels).
+constexpr int kMaxCheckedSeqs = 1 << 16;
+
+// The pool batch of a step call.
+sf_status make_batch(int n_seq, int n_tok, int n_slots, int update, const int* slots,
+                     const int* seq_start, PoolBatch& b) {
   if (n_seq < 0 || n_tok < 0 || n_slots < 0)
     return fail(SF_ERR_INVALID_ARG, "n_seq, n_tok and n_slots must be >= 0");
   // token indices run a staged chunk past the last one in 32 bits
   if (n_tok > (1 << 30)) return fail(SF_ERR_UNSUPPORTED, "n_tok too large");
+  if (update && slots && n_seq > kMaxCheckedSeqs)
+    return fail(SF_ERR_UNSUPPORTED, "more than 65536 sequences with slots and update");
   if (!slots && n_slots < n_seq)
     return fail(SF_ERR_INVALID_ARG, "without slots the pool needs a slot per sequence");
   if (!seq_start && n_seq > 0 && n_tok % n_seq)
@@ -879,7 +887,7 @@ sf_status sf_gdn_recurrent_step(const sf_step_shape* shape, const void* q, const
   // one workgroup takes at least 32 rows of a state; a launch holds 2^32 threads
   if (p.Hv > (1 << 16) || (long long)p.n_seq * p.Hv > (1LL << 21))
     return fail(SF_ERR_UNSUPPORTED, "n_seq * Hv too large");
-  if ((s = make_batch(p.n_seq, p.n_tok, p.n_slots, slots, seq_start, a.b)) != SF_OK) return s;
+  if ((s = make_batch(p.n_seq, p.n_tok, p.n_slots, p.update, slots, seq_start, a.b)) != SF_OK) return s;
   const int D = p.Dk;
   if ((s = token_stride(p.q_stride, (long long)p.Hk * D, "q", &a.qs)) != SF_OK) return s;
   if ((s = token_stride(p.k_stride, (long long)p.Hk * D, "k", &a.ks)) != SF_OK) return s;
@@ -934,7 +942,7 @@ sf_status sf_gdn_shortconv_step(const sf_conv_step_shape* shape, const void* x, 
   if (p.C % 8 || p.C > (1 << 24)) return fail(SF_ERR_UNSUPPORTED, "C must be a multiple of 8, at most 2^24");
   // a launch holds 2^32 threads, one for at least 4 channels of a sequence
   if ((long long)p.n_seq * (p.C + 512) > (1LL << 32)) return fail(SF_ERR_UNSUPPORTED, "n_seq * C too large");
-  if ((s = make_batch(p.n_seq, p.n_tok, p.n_slots, slots, seq_start, a.b)) != SF_OK) return s;
+  if ((s = make_batch(p.n_seq, p.n_tok, p.n_slots, p.update, slots, seq_start, a.b)) != SF_OK) return s;
   if ((s = token_stride(p.x_stride, p.C, "x", &a.xs)) != SF_OK) return s;
   if (p.n_seq == 0 || p.n_tok == 0) return SF_OK;
   if (!x || !w || !y || (p.W > 1 && !state))

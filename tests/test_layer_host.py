@@ -181,3 +181,20 @@ def test_bindings_refuse_cpu_tensors():
                  lambda: gdn.residual_norm_bwd(x, None, None, None, x)):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("call", [_step, _conv])
+def test_checked_slots_are_bounded(call):
+    """The check for repeated slots is quadratic in the sequences: past 65,536
+    of them an updating call with slots is refused.  Without slots, or only
+    reading, nothing is checked.  The output's odd address is refused after
+    that, before any launch."""
+    last = {"o" if call is _step else "y": (16 if call is _step else 6) * G + 2}
+    n = 1 << 16
+    small = dict(Hk=1, Hv=1, Dk=64, Dv=64) if call is _step else dict(C=8)
+    kw = dict(small, n_slots=1 << 21, **last)
+    assert call(n_seq=n + 1, n_tok=n + 1, **kw) == UNS
+    assert "65536" in _lib.load().sf_last_error_message().decode()
+    assert call(n_seq=n, n_tok=n, **kw) == INV
+    assert call(n_seq=n + 1, n_tok=n + 1, update=0, **kw) == INV
+    assert call(n_seq=n + 1, n_tok=n + 1, slots=None, **kw) == INV
