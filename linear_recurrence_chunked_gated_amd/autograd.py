@@ -119,7 +119,8 @@ class _ResidualNorm(torch.autograd.Function):
         y, h = _lib.residual_norm_fwd(x, r, w, s, scale=scale, eps=eps)
         ctx.opts = dict(scale=scale, eps=eps)
         ctx.has_r = r is not None
-        ctx.save_for_backward(h, r if s is not None else None, w, s)
+        ctx.set_materialize_grads(False)  # an unused h: no zeros to write and read
+        ctx.save_for_backward(h, r if ctx.needs_input_grad[3] else None, w, s)
         return (y, h) if ctx.has_r else y
 
     @staticmethod
@@ -127,8 +128,11 @@ class _ResidualNorm(torch.autograd.Function):
     def backward(ctx, dy, dh=None):
         h, r, w, s = ctx.saved_tensors
         need = ctx.needs_input_grad
+        if dy is None and dh is None:
+            return (None,) * 6
+        dy = torch.zeros_like(h) if dy is None else _aligned(dy)
         dx, dr, dw, ds = _lib.residual_norm_bwd(
-            h, r, w, s, _aligned(dy), None if dh is None else _aligned(dh),
+            h, r, w, s, dy, None if dh is None else _aligned(dh),
             want_dr=ctx.has_r and need[1], want_dw=need[2], want_ds=need[3], **ctx.opts)
         return dx, dr, dw, ds, None, None
 

@@ -198,3 +198,56 @@ def test_checked_slots_are_bounded(call):
     assert call(n_seq=n, n_tok=n, **kw) == INV
     assert call(n_seq=n + 1, n_tok=n + 1, update=0, **kw) == INV
     assert call(n_seq=n + 1, n_tok=n + 1, slots=None, **kw) == INV
+
+
+def _residual_autograd(monkeypatch):
+    """residual_norm's autograd over stand-ins for the two calls (h = x + r, y
+    = h; gradients of ones), and what the backward call was given."""
+    from linear_recurrence_chunked_gated_amd import autograd
+    seen = []
+
+    def fwd(x, r, w, s, scale, eps):
+        h = x + r if r is not None else x
+        return h.clone(), h
+
+    def bwd(h, r, w, s, dy, dh, scale, eps, want_dr, want_dw, want_ds):
+        seen.append(dict(r=r, dy=dy, dh=dh, want_ds=want_ds))
+        return (torch.ones_like(h), torch.ones_like(h) if want_dr else None,
+                torch.ones_like(w) if want_dw else None, torch.ones_like(s) if want_ds else None)
+
+    monkeypatch.setattr(_lib, "residual_norm_fwd", fwd)
+    monkeypatch.setattr(_lib, "residual_norm_bwd", bwd)
+    return autograd.residual_norm, seen
+
+
+def _leaves(s_grad=True):
+    x, r = (torch.randn(4, 8).requires_grad_() for _ in range(2))
+    return x, r, torch.ones(8).requires_grad_(), torch.ones(8).requires_grad_(s_grad)
+
+
+def test_residual_norm_backward_of_an_unused_h(monkeypatch):
+    """No tensor of zeros is made for the gradient of an h that nothing used."""
+    norm, seen = _residual_autograd(monkeypatch)
+    y, h = norm(*_leaves())
+    y.sum().backward()
+    assert seen[0]["dh"] is None and (seen[0]["dy"] == 1).all()
+    y, h = norm(*_leaves())
+    (y.sum() + 2 * h.sum()).backward()
+    assert (seen[1]["dh"] == 2).all() and (seen[1]["dy"] == 1).all()
+    # h alone: the norm's part is the gradient of zeros
+    leaves = _leaves()
+    norm(*leaves)[1].sum().backward()
+    assert (seen[2]["dh"] == 1).all() and (seen[2]["dy"] == 0).all()
+    assert seen[2]["dy"].shape == seen[2]["dh"].shape == (4, 8)
+    assert all(t.grad is not None for t in leaves)
+
+
+@pytest.mark.parametrize("s_grad", [True, False])
+def test_residual_norm_keeps_r_for_the_gradient_of_s_only(monkeypatch, s_grad):
+    norm, seen = _residual_autograd(monkeypatch)
+    x, r, w, s = _leaves(s_grad)
+    y, h = norm(x, r, w, s)
+    assert any(t is r for t in y.grad_fn.saved_tensors) == s_grad
+    y.sum().backward()
+    assert seen[0]["want_ds"] == s_grad and (seen[0]["r"] is not None) == s_grad
+    assert (s.grad is not None) == s_grad
