@@ -58,24 +58,27 @@ def _build_calls():
     return r.stdout + r.stderr
 
 
+def _link(objects):
+    tmp = LIB + ".tmp%d" % os.getpid()
+    cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objects
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed: %s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
+    os.replace(tmp, LIB)
+
+
 def build(verbose=False):
     os.makedirs(BUILD, exist_ok=True)
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         calls = ex.submit(_build_calls)
         results = list(ex.map(_compile, SOURCES))
-        results_calls = calls.result()
+        # the library needs hipcc alone: it is there whatever becomes of the module
+        _link([o for o, _ in results])
+        results.append((CALLS, calls.result()))
     if verbose:
         for _, m in results:
             if m.strip():
                 print(m)
-        if results_calls.strip():
-            print(results_calls)
-    tmp = LIB + ".tmp%d" % os.getpid()
-    cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + [o for o, _ in results]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed: %s\n%s%s" % (" ".join(cmd), r.stdout, r.stderr))
-    os.replace(tmp, LIB)
     return LIB
 
 
