@@ -361,7 +361,7 @@ const char* sf_status_string(int status);
 /* Detail of the calling thread's last non-OK status (static until the next
  * failing call on this thread). */
 const char* sf_last_error_message(void);
-/* Library version string. */
+/* Library version string, with a digest of this header as it was built. */
 const char* sf_gdn_version(void);
 
 /* Per-kernel timing for measurement.  sf_gdn_profile_begin(capacity) makes

@@ -472,14 +472,20 @@ def _raise(status, where):
 
 def load_calls():
     """The native module _calls, on the library's entry points (raises if
-    either has not been built)."""
+    either has not been built, or they come from different headers)."""
     global _calls
     if _calls is None:
         lib = load()
-        if not os.path.exists(os.path.join(_HERE, "_calls.so")):
-            raise RuntimeError("_calls.so is not built; run "
-                               "`python -m linear_recurrence_chunked_gated_amd.build`")
-        from . import _calls as module
+        try:
+            from . import _calls as module
+        except ImportError as e:
+            raise RuntimeError("the native module _calls is not built; run "
+                               "`python -m linear_recurrence_chunked_gated_amd.build`") from e
+        version = lib.sf_gdn_version().decode()
+        if not version.endswith("interface %s" % getattr(module, "INTERFACE", None)):
+            raise RuntimeError("%s was not built with this library (%s); rebuild both with "
+                               "`python -m linear_recurrence_chunked_gated_amd.build`"
+                               % (module.__file__, version))
         module.bind(_raise, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
                               for n in _CALL_ENTRIES))
         _calls = module

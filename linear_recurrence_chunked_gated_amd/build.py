@@ -1,11 +1,14 @@
-"""Build libsf_gdn.so (HIP, gfx950) and _calls.so (the native Python calls of
-the layer's operators) in the package directory.
+"""Build libsf_gdn.so (HIP, gfx950) and the module _calls (the native Python
+calls of the layer's operators) in the package directory.
 
     python -m linear_recurrence_chunked_gated_amd.build
 
 Each translation unit is compiled to an object under _build/ in parallel,
-then linked.  Packed-fp32 instruction forms are disabled for device code.
+then linked.  Packed-fp32 instruction forms are disabled for device code.  The
+library and the module are stamped with a digest of the header they share, by
+which the module is matched to the library when it is loaded.
 """
+import hashlib
 import os
 import subprocess
 import sys
@@ -17,7 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libsf_gdn.so")
 SOURCES = ["gdn_fwd.hip", "gdn_bwd.hip", "gdn_conv.hip", "sf_gdn_api.cpp"]
-CALLS = os.path.join(HERE, "_calls.so")
+CALLS = os.path.join(HERE, "_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -27,9 +30,14 @@ CFLAGS = ["-x", "hip", "--offload-arch=" + ARCH, "-O3", "-std=c++17", "-fPIC",
           "-I", os.path.join(HERE, "..", "include")]
 
 
+def _stamp():
+    with open(os.path.join(HERE, "..", "include", "sf_gdn.h"), "rb") as f:
+        return '-DSF_GDN_INTERFACE="%s"' % hashlib.sha256(f.read()).hexdigest()[:16]
+
+
 def _compile(src):
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    cmd = [HIPCC] + CFLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC] + CFLAGS + [_stamp(), "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     msgs = "\n".join(l for l in (r.stdout + r.stderr).splitlines()
                      if "packed-fp32-ops" not in l)
@@ -46,7 +54,7 @@ def _build_calls():
     tmp = CALLS + ".tmp%d" % os.getpid()
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            "-fvisibility=hidden", "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
-           "-I", sysconfig.get_paths()["include"]]
+           _stamp(), "-I", sysconfig.get_paths()["include"]]
     for d in cpp_extension.include_paths():
         cmd += ["-isystem", d]
     cmd += [os.path.join(CSRC, "sf_gdn_calls.cpp"), "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu",

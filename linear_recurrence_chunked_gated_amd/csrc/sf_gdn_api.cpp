@@ -654,7 +654,11 @@ const char* sf_status_string(int status) {
 
 const char* sf_last_error_message(void) { return g_err.c_str(); }
 
-const char* sf_gdn_version(void) { return "sf_gdn 0.1 (gfx950)"; }
+// the header's digest, where the build gives it
+#ifndef SF_GDN_INTERFACE
+#define SF_GDN_INTERFACE "unstamped"
+#endif
+const char* sf_gdn_version(void) { return "sf_gdn 0.1 (gfx950), interface " SF_GDN_INTERFACE; }
 
 sf_status sf_gdn_profile_begin(int capacity) {
   if (capacity <= 0) return fail(SF_ERR_INVALID_ARG, "capacity must be positive");

@@ -552,4 +552,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods};
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__calls() { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__calls() {
+  PyObject* m = PyModule_Create(&module);
+  // the digest of the header whose structs it passes; the library has its own
+  if (m && PyModule_AddStringConstant(m, "INTERFACE", SF_GDN_INTERFACE) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -2,10 +2,13 @@
 stand-ins."""
 import os
 import stat
+import sysconfig
+import types
 
 import pytest
 
-from linear_recurrence_chunked_gated_amd import build
+import linear_recurrence_chunked_gated_amd as gdn
+from linear_recurrence_chunked_gated_amd import _lib, build
 
 
 def _script(path, text):
@@ -41,3 +44,36 @@ def test_a_failed_kernel_leaves_the_old_library(tree, monkeypatch):
     with pytest.raises(RuntimeError, match="compile failed"):
         build.build()
     assert (tree / "lib.so").read_text() == "old"
+
+
+def test_module_is_named_for_its_interpreter():
+    assert os.path.basename(build.CALLS) == "_calls" + sysconfig.get_config_var("EXT_SUFFIX")
+    _lib.load_calls()
+    assert gdn._calls.__file__ == build.CALLS
+
+
+@pytest.mark.parametrize("stamp", [None, "0123456789abcdef"])
+def test_module_of_another_header_is_refused(monkeypatch, stamp):
+    """A module left from another build would pass structs that the library
+    reads differently: it is refused before it is bound."""
+    _lib.load_calls()
+    bound = []
+    old = types.SimpleNamespace(bind=lambda *a: bound.append(a), __file__="old")
+    if stamp:
+        old.INTERFACE = stamp
+    monkeypatch.setattr(_lib, "_calls", None)
+    monkeypatch.setattr(gdn, "_calls", old)
+    with pytest.raises(RuntimeError, match="rebuild"):
+        _lib.load_calls()
+    assert not bound and _lib._calls is None
+
+
+def test_a_missing_module_names_the_build(monkeypatch):
+    """sys.modules holding None makes the import fail as a missing file does."""
+    import sys
+    _lib.load_calls()
+    monkeypatch.setattr(_lib, "_calls", None)
+    monkeypatch.delattr(gdn, "_calls")
+    monkeypatch.setitem(sys.modules, gdn.__name__ + "._calls", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        _lib.load_calls()
