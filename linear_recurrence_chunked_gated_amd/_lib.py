@@ -540,6 +540,10 @@ def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=No
     (None: n_tok / n_seq each).  Returns o [n_tok, Hv, Dv]; rows of padding
     and past the last sequence keep what o held (pass o to set it).
 
+    For decoding only: the output carries no autograd graph, whatever its
+    inputs require.  The pool counts as changed in place, so a graph that has
+    kept its old values raises in its backward.
+
     With ``stream``, here and in the calls below, the kernels run there, in no
     order with the current stream's work but what the caller sets up; outputs
     that the call makes are the given stream's memory."""
@@ -557,7 +561,8 @@ def shortconv_step(x, w, state, slots=None, seq_start=None, act=0, y=None, updat
 
     x [n_tok, C] (token rows may be slices of wider rows), w [C, W] fp32,
     state [n_slots, W-1, C] in x's dtype, advanced in place unless update is
-    False; slots and seq_start as in recurrent_step.  Returns y [n_tok, C]."""
+    False; slots and seq_start, and what it means to autograd, as in
+    recurrent_step.  Returns y [n_tok, C]."""
     f = (_calls or load_calls()).shortconv_step
     args = x, w, state, slots, seq_start, act, y, update
     if stream is None:

@@ -134,6 +134,14 @@ void* out(const Tensor* t) { return t ? t->data_ptr() : nullptr; }
 const float* f32(const Tensor* t) { return (const float*)ptr(t); }
 const int* i32(const Tensor* t) { return (const int*)ptr(t); }
 
+// Tensors that a call has written: autograd counts that as a
+// change in place and refuses values it kept of them.  (Tensors of inference
+// mode have no count.)
+void written(std::initializer_list<const Tensor*> ts) {
+  for (const Tensor* t : ts)
+    if (t && t->defined() && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // Arguments of one call, in the wrapper's order.
 struct Args {
   PyObject* const* a;
@@ -282,6 +290,7 @@ PyObject* recurrent_step(const Args& a) {
     return g_abi.recurrent_step(&s, ptr(q), ptr(k), ptr(v), f32(&alpha), f32(&beta), i32(slots),
                                 i32(seq_start), (float*)out(&state), out(o), st);
   });
+  written({s.update ? &state : nullptr, o});
   return wrap(o);
 }
 
@@ -316,6 +325,7 @@ PyObject* shortconv_step(const Args& a) {
     return g_abi.shortconv_step(&s, ptr(x), f32(&w), i32(slots), i32(seq_start), out(&state),
                                 out(y), st);
   });
+  written({s.update ? &state : nullptr, y});
   return wrap(y);
 }
 
@@ -355,6 +365,7 @@ PyObject* gated_norm_fwd(const Args& a) {
   if (!y) y = &made;
   run(dev, "sf_gdn_gated_norm_fwd",
       [&] { return g_abi.gated_norm_fwd(&s, ptr(x), ptr(gate), f32(w), out(y), st); });
+  written({y});
   return wrap(y);
 }
 
@@ -428,6 +439,7 @@ PyObject* gated_norm_bwd(const Args& a) {
                                 dw.defined() ? (float*)dw.data_ptr() : nullptr,
                                 ws.defined() ? ws.data_ptr() : nullptr, bytes_of(ws), st);
   });
+  written({&dx, &dgate, &dw, &ws});
   return tuple({&dx, &dgate, &dw, &ws});
 }
 
@@ -467,6 +479,7 @@ PyObject* residual_norm_fwd(const Args& a) {
   run(dev, "sf_gdn_residual_norm_fwd", [&] {
     return g_abi.residual_norm_fwd(&sh, ptr(x), ptr(r), f32(s), f32(w), out(h), out(y), st);
   });
+  written({y, h});
   return tuple({y, r ? h : &x});
 }
 
@@ -528,6 +541,7 @@ PyObject* residual_norm_bwd(const Args& a) {
                                    ds.defined() ? (float*)ds.data_ptr() : nullptr,
                                    ws.defined() ? ws.data_ptr() : nullptr, bytes_of(ws), st);
   });
+  written({&dx, &dr, &dw, &ds, &ws});
   return tuple({&dx, &dr, &dw, &ds, &ws});
 }
 

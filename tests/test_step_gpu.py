@@ -477,3 +477,56 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         gdn.shortconv_step(d["q"].view(2, 128), torch.zeros(128, 4, device="cuda"),
                            torch.zeros(3, 2, 128, dtype=torch.bfloat16, device="cuda"))
+
+
+def test_autograd_notices_a_written_pool_and_outputs():
+    """What a call writes counts as written in place: autograd refuses to use a
+    value that it kept of it, and a read-only call does not touch the count."""
+    d = _cuda(step_inputs([1, 1], 2, 2, 64, "bf16", 3, seed=73))
+    args = [d[n] for n in ("q", "k", "v", "alpha", "beta", "state", "slots")]
+    scale = torch.ones_like(d["state"]).requires_grad_()
+    kept = (scale * d["state"]).sum()
+    gdn.recurrent_step(*args, update=False)
+    kept.backward(retain_graph=True)  # the pool as it was
+    gdn.recurrent_step(*args)
+    with pytest.raises(RuntimeError, match="inplace"):
+        kept.backward()
+
+    x, w = torch.randn(3, 64, device="cuda"), torch.randn(64, 4, device="cuda")
+    pool, y = torch.zeros(3, 3, 64, device="cuda"), torch.zeros(3, 64, device="cuda")
+    g = x.view(3, 1, 64)
+    outs = [torch.empty_like(x) for _ in range(5)] + [torch.empty(64, device="cuda")
+                                                      for _ in range(2)]
+    dx, n = torch.empty_like(g), torch.empty_like(g)
+    before = [t._version for t in [pool, y, dx, n] + outs]
+    gdn.shortconv_step(x, w, pool, y=y, update=False)
+    assert pool._version == before[0]
+    gdn.shortconv_step(x, w, pool)
+    gdn.gated_norm_fwd(g, y=n)
+    gdn.gated_norm_bwd(g, None, None, g, grads=(dx, None, None))
+    gdn.residual_norm_fwd(x, x, h=outs[0], y=outs[1])
+    gdn.residual_norm_bwd(x, x, w[:, 0].contiguous(), w[:, 1].contiguous(), x,
+                          grads=(outs[2], outs[3], outs[5], outs[6]))
+    now = [t._version for t in [pool, y, dx, n] + outs]
+    assert all((b > a) == (i != 8) for i, (a, b) in enumerate(zip(before, now)))  # 8: outs[4]
+
+    # a pool made in inference mode has no count, in and out of the mode
+    with torch.inference_mode():
+        pool = d["state"].clone()
+        a = gdn.recurrent_step(*args[:5], pool, d["slots"])
+    want = d["state"].clone()
+    assert torch.equal(a, gdn.recurrent_step(*args[:5], want, d["slots"]))
+    gdn.recurrent_step(*args[:5], pool, d["slots"])
+    gdn.recurrent_step(*args[:5], want, d["slots"])
+    torch.cuda.synchronize()
+    assert torch.equal(pool, want)
+
+
+def test_step_makes_no_graph():
+    d = _cuda(step_inputs([1, 1], 2, 2, 64, "bf16", 3, seed=74))
+    d["v"].requires_grad_()
+    o = gdn.recurrent_step(*(d[n] for n in ("q", "k", "v", "alpha", "beta", "state", "slots")))
+    w = torch.ones(256, 4, device="cuda").requires_grad_()
+    y = gdn.shortconv_step(torch.ones(3, 256, device="cuda"), w,
+                           torch.zeros(3, 3, 256, device="cuda"))
+    assert not o.requires_grad and not y.requires_grad
