@@ -312,6 +312,9 @@ sf_status sf_gdn_shortconv_step(const sf_conv_step_shape* shape, const void* x, 
  * The backward recomputes the statistics from x.  It writes dx, dgate
  * (required with gate) and, unless dw is NULL, dw: the gradient summed over
  * tokens and heads in a fixed order, not accumulated into dw's old contents.
+ * The squares of a row are summed in fp32, which holds for values up to 1e17
+ * (and, with eps = 0, from 1e-16 on).  The sigmoid's relative error grows as
+ * |g| / 2 ulps of fp32, and below 2^-126 it is 0.
  * Only dw needs the workspace (256-byte aligned). */
 typedef struct {
   long long N;
@@ -332,7 +335,8 @@ sf_status sf_gdn_gated_norm_bwd(const sf_gated_norm_shape* shape, const void* x,
  *     h = x + scale * s * r,   y = w * h / sqrt(mean(h^2) + eps)
  * over rows of C values.  s [C] fp32 is a residual scale per channel (NULL:
  * ones), w [C] fp32 (NULL: ones).  r and h may both be NULL: the norm of x
- * alone.  y is formed from h before its rounding to dtype.
+ * alone.  y is formed from h before its rounding to dtype, the backward
+ * starts from h as it was stored.  Squares as in the gated norm.
  *   x, r, h, y, dy, dh, dx, dr [N, C] dtype, contiguous; C a multiple of 8,
  *   at most 16384.
  * The backward takes h as the forward wrote it, dy and dh (the gradient that

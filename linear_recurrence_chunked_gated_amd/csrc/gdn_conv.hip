@@ -306,11 +306,13 @@ __global__ __launch_bounds__(CONV_THREADS) void conv_dw_reduce_kernel(const floa
 // whose loads are issued together, a run ahead (the first one's beside the
 // state's), so that a decoding step waits for memory twice: for the batch's
 // entry, and for all of its inputs.  That latency is what bounds it: 256
-// sequences of 1 to 4 tokens and 6144 channels in bf16 (34.7 MB) take 8.9 us,
-// 19.2 with one token's loads at a time; one sequence of one token 2.2 us.
-// Four channels in bf16 as well, for more waves: eight took 10.4 us there and
-// 15.0 against 10.0 for 16 sequences of 30 tokens, two 8.9 and 7.9, but 3.45
-// against 3.21 for 64 sequences of one.  (The taps by way of LDS, for whole
+// sequences of 1 to 4 tokens and 6144 channels in bf16 (34.7 MB) take 8.9 us
+// replayed from a graph (as all times here), 19.2 with one token's loads at a
+// time; one sequence of one token 2.2 us.  A run waits once more for every
+// four tokens: 16 sequences of 30 tokens and 4096 channels (8.7 MB) 10.0 us.
+// Four channels in bf16 as well, for more waves: eight took 10.4 us on the
+// first and 15.0 on the last, two 8.9 and 7.9, but 3.45 against 3.21 for 64
+// sequences of one token.  (The taps by way of LDS, for whole
 // lines: no gain.)
 constexpr int CONV_STEP_THREADS = 64;
 constexpr int CONV_STEP_RUN = 4;

@@ -18,15 +18,19 @@
 // HBM: every tensor is read and written once, in 16-byte pieces, a row lives
 // in the registers of a group of L lanes between its statistics and its
 // output, and the backward recomputes rstd from x (h), which it reads anyway.
-// Statistics, products and weight gradients are fp32; the outputs in the
-// token type are rounded once.  The forward's y is formed from h before its
+// Statistics, products and weight gradients are fp32 (a mean is the sum times
+// the rounded 1 / n); the outputs in the token type are rounded once.  The forward's y is formed from h before its
 // rounding.
 //
 // In bf16 they run at or above a device copy's 5.1-5.5 TB/s: gated forward of
 // 32,768 tokens x 16 heads x 128 (403 MB) 63.5 us, 6.3 TB/s; gated backward of
 // 62,720 x 16 x 128 (1.28 GB) 216 us and 5 for the sum of dw, 5.8 TB/s;
 // residual forward of 32,768 x 2048 (537 MB) 95 us, 5.6 TB/s, backward (805
-// MB) 145 us and 5, 5.4 TB/s.  Counted HBM bytes are those of the tensors.
+// MB) 145 us and 5, 5.4 TB/s.  In fp32, gated forward of 32,768 x 16 x 128 (805
+// MB) 137 us, 5.9 TB/s, backward (1.34 GB) 252 and 5, 5.2; residual backward of
+// 16,384 x 8192 (3.22 GB) 606 and 5, 5.3, of 8192 x 16,384, whose two pieces a
+// lane leave 32 bytes of spilled registers, 631 and 8, 5.0.  Counted HBM bytes
+// are those of the tensors.
 #pragma once
 #include "gdn_kernels.hpp"
 
@@ -127,8 +131,8 @@ __device__ __forceinline__ float rstd_of(float sum2, float inv_n, float eps) {
   return rsqrtf(sum2 * inv_n + eps);
 }
 
-// sigmoid(g) in the hardware's exponential and reciprocal (an ulp each, the
-// exponent's rounding |g| ulps / 2): the library forms' range handling and
+// sigmoid(g) in the hardware's exponential and reciprocal (an ulp each, and
+// the rounding of the exponent, which costs |g| / 2 ulps of a small result): the library forms' range handling and
 // exact division cost twice the rest of the norm, and the ends are right as
 // they are (exp(-g) = inf gives 0, and what is below 2^-126 may become 0).
 __device__ __forceinline__ float sigmoid(float g) {
@@ -318,7 +322,8 @@ static int norm_lanes(int D) {
 // turn ahead, so that more do not hide more, and each leaves a row of partial
 // weight gradients to write and read again (gated backward of 62,720 x 16 x
 // 128: 384 workgroups 233 us, 512 223, 640 249, 768 224, 1024 243; residual
-// backward of 1021 x 1536 in fp32: 512 13.5 us, 768 15.5, 1024 15.9).
+// backward of 1021 x 1536 in fp32, replayed from a graph with the sum over the
+// partials: 512 13.5 us, 768 15.5, 1024 15.9).
 constexpr int NORM_GROUPS = 512;
 
 int gated_norm_groups(long long N, int H, int D) {

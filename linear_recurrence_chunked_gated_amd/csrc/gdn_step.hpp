@@ -17,7 +17,11 @@
 // value heads at D = 128 (1.08 GB) take 182 us, 5.9 TB/s; a plain device copy
 // of 1 GiB runs at 5.1 TB/s.  64 sequences of 1 to 8 tokens and 16 heads (139
 // MB) take 27 us, 5.1 TB/s.  A long run is bound by a token's dependent
-// arithmetic, 0.24 us: one sequence of 256 tokens takes 62 us.
+// arithmetic, 0.24 us at D = 128 and 0.2 at D = 64: one sequence of 256 tokens
+// (16 heads, D = 128) takes 63 us, 7 of 33 tokens (6 heads, D = 64) 8.4.  Two
+// tokens a reduction would shorten that chain (S_t k_{t+1} = alpha_t S_{t-1}
+// k_{t+1} + u_t k_t . k_{t+1}), but would make a token's bits depend on which
+// tokens came in the same call.
 #pragma once
 #include "gdn_kernels.hpp"
 
@@ -257,8 +261,8 @@ __global__ __launch_bounds__(STEP_THREADS) void recurrent_step_kernel(StepArgs a
         // without a branch between them, and lane i keeps token i's output to
         // store it after the chunk (33 tokens of a 64-wide fp32 state: 7.7 us
         // instead of 8.8).  With many workgroups the late stores cost more
-        // than the branches (64 sequences of 4 tokens in fp32: 54 us instead
-        // of 51).
+        // than the branches (64 sequences of 4 tokens in fp32, 32 heads of
+        // D = 128: 54 us instead of 51).
         static_assert(TB <= L, "a lane for each token's output");
         constexpr int U = 4;
         float out = 0.f;

@@ -888,7 +888,8 @@ sf_status sf_gdn_recurrent_step(const sf_step_shape* shape, const void* q, const
   if (p.Dk != p.Dv || (p.Dk != 64 && p.Dk != 128))
     return fail(SF_ERR_UNSUPPORTED, "Dk == Dv in {64, 128} supported");
   if (p.update != 0 && p.update != 1) return fail(SF_ERR_INVALID_ARG, "update must be 0 or 1");
-  // one workgroup takes at least 32 rows of a state; a launch holds 2^32 threads
+  // a workgroup takes 32 rows of a state, or 16 where there are fewer than 256
+  // such workgroups: at most 2^23 of 256 threads, and a launch holds 2^32
   if (p.Hv > (1 << 16) || (long long)p.n_seq * p.Hv > (1LL << 21))
     return fail(SF_ERR_UNSUPPORTED, "n_seq * Hv too large");
   if ((s = make_batch(p.n_seq, p.n_tok, p.n_slots, p.update, slots, seq_start, a.b)) != SF_OK) return s;
