@@ -536,9 +536,10 @@ def recurrent_step(q, k, v, alpha, beta, state, slots=None, seq_start=None, o=No
     slices of wider rows), alpha, beta [n_tok, Hv] fp32, state [n_slots, Hv,
     Dv, Dk] fp32, advanced in place unless update is False.  slots [n_seq]
     int32 names each sequence's slot (None: sequence i has slot i, one for
-    every slot; negative: padding), seq_start [n_seq + 1] int32 its token rows
-    (None: n_tok / n_seq each).  Returns o [n_tok, Hv, Dv]; rows of padding
-    and past the last sequence keep what o held (pass o to set it).
+    every slot; negative: padding; up to 65,536 of them with update), seq_start
+    [n_seq + 1] int32 its token rows (None: n_tok / n_seq each).  Returns o
+    [n_tok, Hv, Dv]; rows of padding and past the last sequence keep what o
+    held (pass o to set it).
 
     For decoding only: the output carries no autograd graph, whatever its
     inputs require.  The pool counts as changed in place, so a graph that has
