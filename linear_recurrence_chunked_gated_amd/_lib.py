@@ -6,6 +6,11 @@ fallback: if the library is missing or fails, calls raise.  The decoding calls
 and the norms, whose kernels are shorter than their marshalling in Python,
 check and call through the native module _calls (csrc/sf_gdn_calls.cpp) on the
 same entry points.
+
+Every call takes ``stream``, the current one when None.  On another, its
+kernels are in no order with the current stream's work but what the caller sets
+up; outputs that it makes are that stream's memory, marked as used by the
+current one too.
 """
 import ctypes
 import os

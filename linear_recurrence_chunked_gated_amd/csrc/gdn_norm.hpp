@@ -19,8 +19,8 @@
 // in the registers of a group of L lanes between its statistics and its
 // output, and the backward recomputes rstd from x (h), which it reads anyway.
 // Statistics, products and weight gradients are fp32 (a mean is the sum times
-// the rounded 1 / n); the outputs in the token type are rounded once.  The forward's y is formed from h before its
-// rounding.
+// the rounded 1 / n); the outputs in the token type are rounded once.  The
+// forward's y is formed from h before its rounding.
 //
 // In bf16 they run at or above a device copy's 5.1-5.5 TB/s: gated forward of
 // 32,768 tokens x 16 heads x 128 (403 MB) 63.5 us, 6.3 TB/s; gated backward of
@@ -132,9 +132,10 @@ __device__ __forceinline__ float rstd_of(float sum2, float inv_n, float eps) {
 }
 
 // sigmoid(g) in the hardware's exponential and reciprocal (an ulp each, and
-// the rounding of the exponent, which costs |g| / 2 ulps of a small result): the library forms' range handling and
-// exact division cost twice the rest of the norm, and the ends are right as
-// they are (exp(-g) = inf gives 0, and what is below 2^-126 may become 0).
+// the rounding of the exponent, which costs |g| / 2 ulps of a small result):
+// the library forms' range handling and exact division cost twice the rest of
+// the norm, and the ends are right as they are (exp(-g) = inf gives 0, and what
+// is below 2^-126 may become 0).
 __device__ __forceinline__ float sigmoid(float g) {
   return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(g * -1.44269504088896341f));
 }
