@@ -360,6 +360,116 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
                                    const void* dh, void* dx, void* dr, float* dw, float* ds,
                                    void* workspace, size_t ws_bytes, void* stream);
 
+/* Linear attention with a fixed decay for each head, the recurrence of the
+ * chunk calls without the delta rule's correction:
+ *     S_t = a S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t,   a = decay[h]
+ * over whole prompts or training chunks, in fp32 states; a chunk's S_out is the
+ * next one's S_in, and a slot of sf_gdn_decay_step's pool.
+ *
+ * n_tok token rows hold n_seq sequences: n_tok / n_seq rows each (seq_start
+ * NULL), or packed ones of different lengths, sequence i with the rows
+ * seq_start[i] .. seq_start[i+1]-1 (n_seq + 1 offsets in device memory, 4-byte
+ * aligned, which the host does not read: they may be rewritten under a captured
+ * call).  Offsets are clamped to 0 .. n_tok and taken as their running
+ * maximum, so no sequence reaches outside the tensors or into another.  A
+ * sequence may be empty: its state passes through.  Rows of no sequence are
+ * not read, and their outputs keep their contents.
+ *   q, k [n_tok, Hk, Dk], v [n_tok, Hv, Dv] dtype, token rows stride elements
+ *   apart as in the step calls; o, dO, dq, dk, dv contiguous; value head h
+ *   reads q and k of head h / (Hv / Hk); decay [Hv] fp32, any value (meant for
+ *   0 .. 1; 0 keeps each token's own term only); S_in, S_out, dS_out, dS_in
+ *   [n_seq, Hv, Dv, Dk] fp32.  NULL S_in / dS_out mean zeros; NULL S_out /
+ *   dS_in mean not wanted.
+ * The backward writes the gradients of <dO, o> + <dS_out, S_out> in q, k
+ * (summed over the value heads of a key head, in order), v and S_in.  The decay
+ * is a constant of the layer and gets none.
+ *
+ * In bf16 the masked products q k^T and the state's copy that meets q are
+ * rounded to bf16 on the way to o (as the operands of its products), the
+ * states are not (2^-17).  fp32 tensors enter the products as pairs of bf16
+ * (2^-17 of a term; o, the states and the gradients within about 1e-5 of
+ * their norm).  Finite inputs are a precondition: a value that is not finite
+ * reaches the outputs of its 64-token block and of the later ones (earlier
+ * ones, for gradients) of its sequence, and no other sequence.
+ *
+ * The workspace (256-byte aligned) holds the table of segments and the states
+ * at their boundaries, and for shared key heads in the backward 8 bytes for
+ * each element of v.  Calls that may run at the same time need one each.
+ * Dk == Dv in {64, 128}; n_tok up to 2^30, n_seq * Hv up to 2^21. */
+typedef struct {
+  int n_seq, n_tok;
+  int Hk, Hv;
+  int Dk, Dv;
+  int dtype;
+  float scale;
+  long long q_stride, k_stride, v_stride;
+} sf_decay_shape;
+sf_status sf_gdn_decay_chunk_fwd_workspace_size(const sf_decay_shape* shape, size_t* bytes);
+sf_status sf_gdn_decay_chunk_bwd_workspace_size(const sf_decay_shape* shape, size_t* bytes);
+sf_status sf_gdn_decay_chunk_fwd(const sf_decay_shape* shape, const void* q, const void* k,
+                                 const void* v, const float* decay, const int* seq_start,
+                                 const float* S_in, void* o, float* S_out, void* workspace,
+                                 size_t ws_bytes, void* stream);
+sf_status sf_gdn_decay_chunk_bwd(const sf_decay_shape* shape, const void* q, const void* k,
+                                 const void* v, const float* decay, const int* seq_start,
+                                 const float* S_in, const void* dO, const float* dS_out, void* dq,
+                                 void* dk, void* dv, float* dS_in, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
+/* The same recurrence by single tokens over a pool of states, a batch as in
+ * sf_gdn_recurrent_step (slots, seq_start, padding, refused entries, limits),
+ * in fp32 throughout.  A sequence's outputs and state are the same, bit for
+ * bit, whatever else is in the batch and however its tokens are spread over
+ * calls.  state [n_slots, Hv, Dv, Dk] fp32, in place; decay [Hv] fp32. */
+typedef struct {
+  int n_seq, n_tok, n_slots;
+  int Hk, Hv;
+  int Dk, Dv;
+  int dtype;
+  int update;
+  float scale;
+  long long q_stride, k_stride, v_stride;
+} sf_decay_step_shape;
+sf_status sf_gdn_decay_step(const sf_decay_step_shape* shape, const void* q, const void* k,
+                            const void* v, const float* decay, const int* slots,
+                            const int* seq_start, float* state, void* o, void* stream);
+
+/* Norm of every query and key head with the rotation by position in the same
+ * pass:
+ *     z = scale * w * x / sqrt(mean(x^2) + eps),   y = R(pos) z
+ * R turns F pairs of z's first 2 F values by the angle pos * freq[i]:
+ *     (y1, y2) = (z1 cos - z2 sin, z2 cos + z1 sin)
+ * with pairs (i, i + F) (neighbours = 0) or (2 i, 2 i + 1) (neighbours = 1);
+ * values past them are not turned.
+ *   q [N, Hq, D], k [N, Hk, D] dtype, token rows q_stride (k_stride) elements
+ *   apart (0: contiguous; a multiple of 8); yq, yk, dyq, dyk, dq, dk
+ *   contiguous; wq, wk [D] fp32 (NULL: ones), each with a scale of its own; pos
+ *   [N] int32 (NULL: first + n % T for row n); freq [F] fp32.
+ *   D a multiple of 8, at most 512; 2 F <= D, F a multiple of 8 (of 4 with
+ *   neighbours; 0: no rotation, freq NULL).
+ * Angles are reduced to a fraction of a turn in 64 bits, for any int32
+ * position.  The backward recomputes the statistics; dwq and dwk (NULL: not
+ * wanted) are summed over tokens and heads in a fixed order, not accumulated,
+ * and need the workspace (256-byte aligned).  Squares as in the gated norm. */
+typedef struct {
+  long long N, T;
+  int Hq, Hk, D, F;
+  int dtype;
+  int neighbours;
+  int first;
+  float eps, q_scale, k_scale;
+  long long q_stride, k_stride;
+} sf_rotary_shape;
+sf_status sf_gdn_qk_norm_rotary_fwd(const sf_rotary_shape* shape, const void* q, const void* k,
+                                    const int* pos, const float* freq, const float* wq,
+                                    const float* wk, void* yq, void* yk, void* stream);
+sf_status sf_gdn_qk_norm_rotary_bwd_workspace_size(const sf_rotary_shape* shape, size_t* bytes);
+sf_status sf_gdn_qk_norm_rotary_bwd(const sf_rotary_shape* shape, const void* q, const void* k,
+                                    const int* pos, const float* freq, const float* wq,
+                                    const float* wk, const void* dyq, const void* dyk, void* dq,
+                                    void* dk, float* dwq, float* dwk, void* workspace,
+                                    size_t ws_bytes, void* stream);
+
 /* Static text for a status code. */
 const char* sf_status_string(int status);
 /* Detail of the calling thread's last non-OK status (static until the next

@@ -67,6 +67,30 @@ class ResidualNormShape(ctypes.Structure):
                 ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
 
 
+class DecayShape(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int), ("n_tok", ctypes.c_int), ("Hk", ctypes.c_int),
+                ("Hv", ctypes.c_int), ("Dk", ctypes.c_int), ("Dv", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float),
+                ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong),
+                ("v_stride", ctypes.c_longlong)]
+
+
+class DecayStepShape(ctypes.Structure):
+    _fields_ = [("n_seq", ctypes.c_int), ("n_tok", ctypes.c_int), ("n_slots", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("Hv", ctypes.c_int), ("Dk", ctypes.c_int),
+                ("Dv", ctypes.c_int), ("dtype", ctypes.c_int), ("update", ctypes.c_int),
+                ("scale", ctypes.c_float), ("q_stride", ctypes.c_longlong),
+                ("k_stride", ctypes.c_longlong), ("v_stride", ctypes.c_longlong)]
+
+
+class RotaryShape(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_longlong), ("T", ctypes.c_longlong), ("Hq", ctypes.c_int),
+                ("Hk", ctypes.c_int), ("D", ctypes.c_int), ("F", ctypes.c_int),
+                ("dtype", ctypes.c_int), ("neighbours", ctypes.c_int), ("first", ctypes.c_int),
+                ("eps", ctypes.c_float), ("q_scale", ctypes.c_float), ("k_scale", ctypes.c_float),
+                ("q_stride", ctypes.c_longlong), ("k_stride", ctypes.c_longlong)]
+
+
 SIGNATURES = {
     "sf_gdn_chunk_fwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.POINTER(_sz)]),
     "sf_gdn_chunk_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(Shape), ctypes.POINTER(_sz)]),
@@ -99,6 +123,18 @@ SIGNATURES = {
                                                                ctypes.POINTER(_sz)]),
     "sf_gdn_residual_norm_bwd": (ctypes.c_int, [ctypes.POINTER(ResidualNormShape)] + [_vp] * 11
                                  + [_sz, _vp]),
+    "sf_gdn_decay_chunk_fwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(DecayShape),
+                                                             ctypes.POINTER(_sz)]),
+    "sf_gdn_decay_chunk_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(DecayShape),
+                                                             ctypes.POINTER(_sz)]),
+    "sf_gdn_decay_chunk_fwd": (ctypes.c_int, [ctypes.POINTER(DecayShape)] + [_vp] * 9 + [_sz, _vp]),
+    "sf_gdn_decay_chunk_bwd": (ctypes.c_int, [ctypes.POINTER(DecayShape)] + [_vp] * 13 + [_sz, _vp]),
+    "sf_gdn_decay_step": (ctypes.c_int, [ctypes.POINTER(DecayStepShape)] + [_vp] * 9),
+    "sf_gdn_qk_norm_rotary_fwd": (ctypes.c_int, [ctypes.POINTER(RotaryShape)] + [_vp] * 9),
+    "sf_gdn_qk_norm_rotary_bwd_workspace_size": (ctypes.c_int, [ctypes.POINTER(RotaryShape),
+                                                                ctypes.POINTER(_sz)]),
+    "sf_gdn_qk_norm_rotary_bwd": (ctypes.c_int, [ctypes.POINTER(RotaryShape)] + [_vp] * 13
+                                  + [_sz, _vp]),
     "sf_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "sf_last_error_message": (ctypes.c_char_p, []),
     "sf_gdn_version": (ctypes.c_char_p, []),
@@ -468,7 +504,11 @@ _calls = None
 _CALL_ENTRIES = ("sf_gdn_recurrent_step", "sf_gdn_shortconv_step", "sf_gdn_gated_norm_fwd",
                  "sf_gdn_gated_norm_bwd", "sf_gdn_gated_norm_bwd_workspace_size",
                  "sf_gdn_residual_norm_fwd", "sf_gdn_residual_norm_bwd",
-                 "sf_gdn_residual_norm_bwd_workspace_size")
+                 "sf_gdn_residual_norm_bwd_workspace_size", "sf_gdn_decay_chunk_fwd",
+                 "sf_gdn_decay_chunk_fwd_workspace_size", "sf_gdn_decay_chunk_bwd",
+                 "sf_gdn_decay_chunk_bwd_workspace_size", "sf_gdn_decay_step",
+                 "sf_gdn_qk_norm_rotary_fwd", "sf_gdn_qk_norm_rotary_bwd",
+                 "sf_gdn_qk_norm_rotary_bwd_workspace_size")
 
 
 def _raise(status, where):
@@ -643,6 +683,102 @@ def residual_norm_bwd(h, r, w, s, dy, dh=None, scale=1.0, eps=1e-6, grads=None, 
     if stream is None:
         return f(*args, _raw_stream(h))[:4]
     return _call_on(stream, h, f, *args,
+                    made=lambda got: got[:4] if grads is None else ())[:4]
+
+
+def decay_chunk_fwd(q, k, v, decay, S_in=None, seq_start=None, scale=1.0, o=None, S_out=None,
+                    workspace=None, stream=None):
+    """sf_gdn_decay_chunk_fwd on torch tensors: linear attention with a fixed
+    decay for each head, S_t = decay S_{t-1} + v_t k_t^T and o_t = scale S_t
+    q_t, over whole sequences.  Returns (o, S_out).
+
+    q, k [B, T, Hk, Dk] and v [B, T, Hv, Dv], or packed sequences: [n_tok, Hk,
+    Dk] and [n_tok, Hv, Dv] with seq_start [n_seq + 1] int32 offsets on the
+    device (without it: one sequence).  bf16 or fp32; token rows may be slices
+    of wider rows; value head h reads q and k of head h // (Hv // Hk).  decay
+    [Hv] fp32; S_in (None: zeros) and S_out [B or n_seq, Hv, Dv, Dk] fp32, as
+    in chunk_fwd and as the slots of decay_step's pool.  Rows of no sequence
+    keep what o held (pass o to set it)."""
+    f = (_calls or load_calls()).decay_chunk_fwd
+    args = q, k, v, decay, S_in, seq_start, scale, o, S_out, workspace
+    if stream is None:
+        return f(*args, _raw_stream(q))[:2]
+    return _call_on(stream, q, f, *args,
+                    made=lambda got: (None if o is not None else got[0],
+                                      None if S_out is not None else got[1]))[:2]
+
+
+def decay_chunk_bwd(q, k, v, decay, S_in, dO, dS_out=None, seq_start=None, scale=1.0, grads=None,
+                    want_dS_in=True, workspace=None, stream=None):
+    """sf_gdn_decay_chunk_bwd on torch tensors: the gradients of <dO, o> +
+    <dS_out, S_out> (dS_out None: zeros).  Returns (dq, dk, dv, dS_in); dS_in
+    is None with want_dS_in False.  ``grads`` may supply preallocated outputs
+    in that order.  The decay is a constant and gets no gradient; rows of no
+    sequence keep what dq, dk and dv held."""
+    f = (_calls or load_calls()).decay_chunk_bwd
+    args = q, k, v, decay, S_in, dO, dS_out, seq_start, scale, grads, want_dS_in, workspace
+    if stream is None:
+        return f(*args, _raw_stream(q))[:4]
+    return _call_on(stream, q, f, *args,
+                    made=lambda got: got[:4] if grads is None else ())[:4]
+
+
+def decay_step(q, k, v, decay, state, slots=None, seq_start=None, o=None, update=True, scale=1.0,
+               stream=None):
+    """sf_gdn_decay_step on torch tensors: the recurrence of decay_chunk_fwd
+    token by token over a pool of states, for decoding.
+
+    q, k [n_tok, Hk, Dk], v [n_tok, Hv, Dv] (bf16 or fp32), decay [Hv] fp32;
+    state [n_slots, Hv, Dv, Dk] fp32, advanced in place unless update is False;
+    slots, seq_start, o, padding, refused entries and what it means to autograd
+    as in recurrent_step.  Returns o [n_tok, Hv, Dv]."""
+    f = (_calls or load_calls()).decay_step
+    args = q, k, v, decay, state, slots, seq_start, o, update, scale
+    if stream is None:
+        return f(*args, _raw_stream(q))
+    return _call_on(stream, q, f, *args, made=None if o is None else _none)
+
+
+_PAIRS = {"halves": False, "neighbours": True}
+
+
+def _neighbours(pairs):
+    if pairs not in _PAIRS:
+        raise ValueError("pairs must be 'halves' or 'neighbours', got %r" % (pairs,))
+    return _PAIRS[pairs]
+
+
+def qk_norm_rotary_fwd(q, k, pos=None, freq=None, wq=None, wk=None, eps=1e-6, q_scale=1.0,
+                       k_scale=1.0, pairs="halves", first=0, yq=None, yk=None, stream=None):
+    """sf_gdn_qk_norm_rotary_fwd on torch tensors: every head of q [..., T, Hq,
+    D] and k [..., T, Hk, D] as scale * w * x / sqrt(mean(x^2) + eps), its first
+    2 F values turned in pairs by the angles pos * freq.  Returns (yq, yk).
+
+    pos int32, the shape before the heads (None: first, first + 1, .. along T);
+    freq [F] fp32 (None: no rotation); wq, wk [D] fp32 or None (ones); pairs
+    "halves" (i with i + F) or "neighbours" (2 i with 2 i + 1).  q and k may be
+    head slices of wider token rows."""
+    f = (_calls or load_calls()).qk_norm_rotary_fwd
+    args = q, k, pos, freq, wq, wk, eps, q_scale, k_scale, _neighbours(pairs), first, yq, yk
+    if stream is None:
+        return f(*args, _raw_stream(q))
+    return _call_on(stream, q, f, *args,
+                    made=lambda got: (None if yq is not None else got[0],
+                                      None if yk is not None else got[1]))
+
+
+def qk_norm_rotary_bwd(q, k, pos, freq, wq, wk, dyq, dyk, eps=1e-6, q_scale=1.0, k_scale=1.0,
+                       pairs="halves", first=0, grads=None, want_dw=True, workspace=None,
+                       stream=None):
+    """sf_gdn_qk_norm_rotary_bwd on torch tensors.  Returns (dq, dk, dwq, dwk),
+    with None for the gradient of a weight that is None (of both with want_dw
+    False).  ``grads`` may supply preallocated outputs in that order."""
+    f = (_calls or load_calls()).qk_norm_rotary_bwd
+    args = (q, k, pos, freq, wq, wk, dyq, dyk, eps, q_scale, k_scale, _neighbours(pairs), first,
+            grads, want_dw, workspace)
+    if stream is None:
+        return f(*args, _raw_stream(q))[:4]
+    return _call_on(stream, q, f, *args,
                     made=lambda got: got[:4] if grads is None else ())[:4]
 
 

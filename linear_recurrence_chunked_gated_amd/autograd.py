@@ -4,6 +4,8 @@
     short_conv(x, w, conv_in=None, act=0)                           -> (y, conv_out)
     gated_norm(x, gate=None, w=None, eps, scale, act)               -> y
     residual_norm(x, r=None, w=None, s=None, scale, eps)            -> (y, h)
+    decay_chunk(q, k, v, decay, S_in=None, seq_start=None, scale)   -> (o, S_out)
+    qk_norm_rotary(q, k, pos=None, freq=None, wq=None, wk=None, ..) -> (yq, yk)
 
 The forward is the saving forward (sf_gdn_chunk_fwd_save: o and S_out, with
 each block's entry state and V^new kept for the backward), and the backward is
@@ -15,7 +17,10 @@ sequence.  short_conv is the causal depthwise convolution ahead of the
 recurrence (sf_gdn_shortconv_fwd / _bwd), whose W-1-token boundary state
 chains the same way.  gated_norm and residual_norm are the layer's norms after
 and before the recurrence (sf_gdn_gated_norm_*, sf_gdn_residual_norm_*); their
-backward keeps no statistics, it forms them again from x (h).  A backward
+backward keeps no statistics, it forms them again from x (h).  decay_chunk is
+linear attention with a fixed decay for each head (sf_gdn_decay_chunk_*), whose
+backward forms the states again; qk_norm_rotary the norm and rotation of its
+queries and keys (sf_gdn_qk_norm_rotary_*).  A backward
 pass captured into a HIP graph needs every earlier autograd graph of the same
 leaves gone (torch orders their gradients with the stream that those ran on,
 which a capture does not allow).  Argument marshalling only: both passes are the library's
@@ -146,3 +151,77 @@ def residual_norm(x, r=None, w=None, s=None, scale=1.0, eps=1e-6):
             raise ValueError("s needs r")
         return _ResidualNorm.apply(x, None, w, None, scale, eps), x
     return _ResidualNorm.apply(x, r, w, s, scale, eps)
+
+
+class _DecayChunk(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, decay, S_in, seq_start, scale):
+        # rows of no sequence: zeros, and zeros for their gradients
+        o = None if seq_start is None else v.new_zeros(v.shape)
+        o, S_out = _lib.decay_chunk_fwd(q, k, v, decay, S_in, seq_start, scale, o=o)
+        ctx.save_for_backward(q, k, v, decay, S_in, seq_start)
+        ctx.scale = scale
+        ctx.set_materialize_grads(False)
+        return o, S_out
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dO, dS_out):
+        q, k, v, decay, S_in, seq_start = ctx.saved_tensors
+        if dO is None and dS_out is None:
+            return (None,) * 7
+        want = ctx.needs_input_grad[4]
+        dO = v.new_zeros(v.shape) if dO is None else _aligned(dO)
+        grads = None
+        if seq_start is not None:
+            grads = (q.new_zeros(q.shape), k.new_zeros(k.shape), v.new_zeros(v.shape),
+                     torch.empty_like(S_in) if want else None)
+        dq, dk, dv, dS_in = _lib.decay_chunk_bwd(
+            q, k, v, decay, S_in, dO, None if dS_out is None else _aligned(dS_out), seq_start,
+            ctx.scale, grads=grads, want_dS_in=want)
+        return dq, dk, dv, None, dS_in, None, None
+
+
+def decay_chunk(q, k, v, decay, S_in=None, seq_start=None, scale=1.0):
+    """(o, S_out) of linear attention with a fixed decay for each head,
+    differentiable in q, k, v and S_in; arguments as in decay_chunk_fwd.  The
+    decay is a constant: one that requires a gradient is refused.  Rows of no
+    sequence are zeros in o, and in the gradients."""
+    if decay.requires_grad:
+        raise ValueError("decay is a constant of the layer and has no gradient")
+    return _DecayChunk.apply(q, k, v, decay, S_in, seq_start, scale)
+
+
+class _QkNormRotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, pos, freq, wq, wk, opts):
+        yq, yk = _lib.qk_norm_rotary_fwd(q, k, pos, freq, wq, wk, **opts)
+        ctx.save_for_backward(q, k, pos, freq, wq, wk)
+        ctx.opts = opts
+        ctx.set_materialize_grads(False)
+        return yq, yk
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dyq, dyk):
+        q, k, pos, freq, wq, wk = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        if dyq is None and dyk is None:
+            return (None,) * 7
+        dyq = q.new_zeros(q.shape) if dyq is None else _aligned(dyq)
+        dyk = k.new_zeros(k.shape) if dyk is None else _aligned(dyk)
+        dq, dk, dwq, dwk = _lib.qk_norm_rotary_bwd(q, k, pos, freq, wq, wk, dyq, dyk,
+                                                   want_dw=need[4] or need[5], **ctx.opts)
+        return dq, dk, None, None, dwq, dwk, None
+
+
+def qk_norm_rotary(q, k, pos=None, freq=None, wq=None, wk=None, eps=1e-6, q_scale=1.0, k_scale=1.0,
+                   pairs="halves", first=0):
+    """(yq, yk): every head's norm with the rotation by position,
+    differentiable in q, k, wq and wk; arguments as in qk_norm_rotary_fwd.
+    freq is a constant: one that requires a gradient is refused."""
+    if freq is not None and freq.requires_grad:
+        raise ValueError("freq is a constant of the layer and has no gradient")
+    return _QkNormRotary.apply(q, k, pos, freq, wq, wk,
+                               dict(eps=eps, q_scale=q_scale, k_scale=k_scale, pairs=pairs,
+                                    first=first))

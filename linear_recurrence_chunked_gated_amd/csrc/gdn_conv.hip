@@ -16,9 +16,11 @@
 // with the W-1 previous inputs in registers, so every input is read once.
 //
 // This unit also compiles the other streaming kernels of a layer: the
-// single-token recurrence (gdn_step.hpp) and the norms (gdn_norm.hpp).
+// single-token recurrences (gdn_step.hpp) and the norms (gdn_norm.hpp,
+// gdn_rotary.hpp).
 #include "gdn_kernels.hpp"
 #include "gdn_norm.hpp"
+#include "gdn_rotary.hpp"
 #include "gdn_step.hpp"
 
 namespace sfgdn {

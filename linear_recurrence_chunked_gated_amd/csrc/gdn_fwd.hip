@@ -19,6 +19,9 @@
 // "What carries the argument") applied inside one chunk so that the low
 // parallelism of the state transition (Figure 2 caption; "grid-size tuning")
 // does not leave the GPU idle: P segments give B*H*P workgroups.
+//
+// This unit also compiles linear attention with a decay (gdn_decay.hpp).
+#include "gdn_decay.hpp"
 #include "gdn_kernels.hpp"
 
 namespace sfgdn {

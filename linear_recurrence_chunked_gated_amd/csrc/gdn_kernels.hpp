@@ -183,6 +183,120 @@ struct ResidualNormArgs {
 int gated_norm_groups(long long N, int H, int D);
 int residual_norm_groups(long long N, int C);
 
+// Linear attention with a decay for each head (see gdn_decay.hpp).
+//
+// A call's segments.  Sequences of one length (table null): T tokens in P
+// segments of L.  Packed ones: a table of ints on the device, written by the
+// call's first kernel,
+//   [0] items, [1] sequences of several segments, [2], [3] the rows they have,
+//   max_items items of {sequence, first token, tokens, boundary slots before
+//   and after it (-1: none)}, max_multi of {sequence, first boundary slot,
+//   boundaries, tokens of the last segment}.
+constexpr int kDecayHead = 4, kDecayItem = 5, kDecayMulti = 4;
+struct DecayPlan {
+  int* table;
+  int L, T, P;
+  int max_items, max_multi;
+};
+struct DecayTensor {
+  const void* p;
+  long long stride;  // elements between token rows
+  int shared;        // heads of the key kind: one for each group of value heads
+};
+// One scan: the roles of its tensors; y [n_tok, Hv, D] in the token type or
+// fp32; states [.., D, D] as [w index][u index], or transposed.
+struct DecayRole {
+  DecayTensor x, u, w;
+  void* y;
+  int y_f32;
+  float* bound;        // [slots][Hv][D][D] at the inner boundaries
+  const float* state;  // [n_seq][Hv][D][D] before the first block, or null (zeros)
+  float* exit;         // the same after the last one, or null
+  float s_out, s_pair;  // factors of y, and of every product w u
+  int tr_state, tr_bound;
+};
+struct DecayScanArgs {
+  DecayPlan plan;
+  const float* decay;  // [Hv]
+  int Hv, group;
+  DecayRole role[2];
+};
+struct DecayChainRole {
+  float* bound;
+  const float* state;
+  int tr_state, rev;
+};
+struct DecayChainArgs {
+  DecayPlan plan;
+  const float* decay;
+  int Hv;
+  DecayChainRole role[2];
+};
+struct DecayGroupArgs {
+  DecayPlan plan;
+  const float* part[2];  // [n_tok][Hv][D]
+  void* y[2];            // [n_tok][Hk][D]
+  int n_tok, Hk, group;
+};
+struct DecayArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* decay;
+  const int* seq_start;
+  const float* S_in;
+  void* o;
+  float* S_out;
+  const void* dO;
+  const float* dS_out;
+  void* dq;
+  void* dk;
+  void* dv;
+  float* dS_in;
+  long long qs, ks, vs;
+  int n_seq, n_tok, Hv, group;
+  float scale;
+  // workspace
+  DecayPlan plan;
+  float* bound[2];
+  float* part[2];  // backward with shared heads: each value head's dq and dk
+};
+
+// The same recurrence by single tokens over a pool (see gdn_step.hpp).
+struct DecayStepArgs {
+  PoolBatch b;
+  const void* q;
+  const void* k;
+  const void* v;
+  const float* decay;
+  float* state;
+  void* o;
+  long long qs, ks, vs;
+  int Hv, group, update;
+  float scale;
+};
+
+// Norm and rotation of queries and keys (see gdn_rotary.hpp): N tokens of
+// H[0] query and H[1] key heads of D values; F pairs turned by pos * freq.
+// y: forward the outputs, backward the gradients dx, contiguous.
+struct RotaryArgs {
+  const void* x[2];
+  long long xs[2];
+  const float* w[2];   // null: ones
+  const void* dy[2];
+  void* y[2];
+  float scale[2];
+  int H[2];
+  const int* pos;      // null: first + token % T
+  const float* freq;   // [F]
+  float* part;         // backward: [groups][D] for each weight gradient wanted (dw[0], then dw[1])
+  float* dw[2];
+  long long N, T;
+  int D, F, first;
+  float eps;
+};
+int rotary_groups(long long N);
+
 // Optional per-launch event timing (see sf_gdn_profile_* in the C ABI).
 struct Profiler;
 void prof_begin(Profiler* p, const char* name, hipStream_t st);
@@ -226,7 +340,18 @@ template <typename T, int D>
 hipError_t launch_recurrent_step(const StepArgs& a, hipStream_t st, Profiler* prof);
 template <typename T>
 hipError_t launch_conv_step(const ConvStepArgs& a, hipStream_t st, Profiler* prof);
+template <typename T, int D>
+hipError_t launch_decay_step(const DecayStepArgs& a, hipStream_t st, Profiler* prof);
+// Linear attention with a decay for each head.
+template <typename T, int D>
+hipError_t launch_decay_fwd(const DecayArgs& a, hipStream_t st, Profiler* prof);
+template <typename T, int D>
+hipError_t launch_decay_bwd(const DecayArgs& a, hipStream_t st, Profiler* prof);
 // Norms.
+template <typename T>
+hipError_t launch_rotary_fwd(const RotaryArgs& a, bool neighbours, hipStream_t st, Profiler* prof);
+template <typename T>
+hipError_t launch_rotary_bwd(const RotaryArgs& a, bool neighbours, hipStream_t st, Profiler* prof);
 template <typename T>
 hipError_t launch_gated_norm_fwd(const GatedNormArgs& a, hipStream_t st, Profiler* prof);
 template <typename T>

@@ -343,4 +343,153 @@ template hipError_t launch_recurrent_step<bf16, 128>(const StepArgs&, hipStream_
 template hipError_t launch_recurrent_step<float, 64>(const StepArgs&, hipStream_t, Profiler*);
 template hipError_t launch_recurrent_step<float, 128>(const StepArgs&, hipStream_t, Profiler*);
 
+// ------------------------------------------- linear attention with a decay
+// The recurrence of gdn_decay.hpp one token at a time over the same kind of
+// pool:
+//     S <- a S + v k^T,   o = scale S q
+// laid out as above, a row of the state on eight lanes.  A token's update does
+// not wait for a sum over the row: only its output does, so tokens overlap.
+// One token per sequence is bound by the states' traffic.
+template <typename T, int D, bool SINGLE, bool STREAM>
+__global__ __launch_bounds__(STEP_THREADS) void decay_step_kernel(DecayStepArgs a) {
+  constexpr int L = 8, NE = D / (4 * L), WROWS = 64 / L, ROWS = 4 * WROWS, PARTS = D / ROWS;
+  typedef T vec4 __attribute__((ext_vector_type(4)));
+  const int part = blockIdx.x % PARTS;
+  const int sh = blockIdx.x / PARTS;
+  const int hv = sh % a.Hv, seq = sh / a.Hv;
+  const SeqEntry e = seq_entry(a.b, seq);
+  if (e.slot < 0 || e.t0 >= e.t1) return;
+  const int lane = lane_id(), l = lane % L;
+  const int wrow = wave_id() * WROWS + lane / L;  // this lane's row in the workgroup
+  const int r0 = part * ROWS;
+  T* __restrict__ o = reinterpret_cast<T*>(a.o) + (size_t)hv * D + r0 + wrow;
+  const size_t os = (size_t)a.Hv * D;
+
+  f32x4 S[NE];
+  float* Sp = a.state;
+  if (!e.bad) {
+    Sp += ((size_t)e.slot * a.Hv + hv) * D * D + (size_t)(r0 + wrow) * D + l * 4;
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      const f32x4* p = reinterpret_cast<const f32x4*>(Sp + j * 4 * L);
+      S[j] = STREAM ? __builtin_nontemporal_load(p) : *p;
+    }
+  }
+  const bool bad = e.bad || (a.update && a.b.slots && slot_repeats<4>(a.b, seq, e.slot));
+  if (bad) {
+    if (l == 0)
+      for (int t = e.t0; t < e.t1; ++t) o[t * os] = (T)__builtin_nanf("");
+    return;
+  }
+  const int hk = hv / a.group;
+  const T* __restrict__ q = reinterpret_cast<const T*>(a.q) + (size_t)hk * D;
+  const T* __restrict__ k = reinterpret_cast<const T*>(a.k) + (size_t)hk * D;
+  const T* __restrict__ v = reinterpret_cast<const T*>(a.v) + (size_t)hv * D + r0;
+  const float alpha = a.decay[hv];
+
+  // which products are fused is written out: a token's bits do not depend on
+  // the tokens beside it
+  auto token = [&](const f32x4 (&x)[NE], const f32x4 (&y)[NE], float vt) {
+#pragma unroll
+    for (int j = 0; j < NE; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[j][i] = __builtin_fmaf(vt, x[j][i], alpha * S[j][i]);
+    return a.scale * row_dot<NE, L>(S, y);
+  };
+
+  if constexpr (SINGLE) {
+    const size_t t = e.t0;
+    f32x4 x[NE], y[NE];
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      x[j] = __builtin_convertvector(
+          *reinterpret_cast<const vec4*>(k + t * a.ks + (j * L + l) * 4), f32x4);
+      y[j] = __builtin_convertvector(
+          *reinterpret_cast<const vec4*>(q + t * a.qs + (j * L + l) * 4), f32x4);
+    }
+    const float r = token(x, y, (float)v[t * a.vs + wrow]);
+    if (l == 0) o[t * os] = (T)r;
+  } else {
+    // tokens staged through LDS a chunk ahead, as in the step above
+    constexpr int TT = step_token_threads(D), TB = step_tokens(D);
+    constexpr int VV = (ROWS + TT - 1) / TT;
+    struct Chunk {
+      f32x4 k[TB][D / 4], q[TB][D / 4];
+      float v[TB][VV * TT];
+    };
+    __shared__ Chunk lds[2];
+    const int st = threadIdx.x / TT, sl = threadIdx.x % TT;  // token of the chunk, unit in it
+    vec4 rk, rq;
+    T rv[VV];
+    auto load = [&](int c) {
+      const size_t t = min(c + st, e.t1 - 1);  // past the end: the last token again, not used
+      rk = *reinterpret_cast<const vec4*>(k + t * a.ks + sl * 4);
+      rq = *reinterpret_cast<const vec4*>(q + t * a.qs + sl * 4);
+#pragma unroll
+      for (int i = 0; i < VV; ++i) rv[i] = v[t * a.vs + min(i * TT + sl, ROWS - 1)];
+    };
+    T* ot = o + e.t0 * os;
+    load(e.t0);
+#pragma unroll 1
+    for (int c = e.t0, buf = 0; c < e.t1; c += TB, buf ^= 1) {
+      // this buffer's readers (two chunks back) have passed the last barrier
+      Chunk& b = lds[buf];
+      b.k[st][sl] = __builtin_convertvector(rk, f32x4);
+      b.q[st][sl] = __builtin_convertvector(rq, f32x4);
+#pragma unroll
+      for (int i = 0; i < VV; ++i) b.v[st][i * TT + sl] = (float)rv[i];
+      __syncthreads();
+      if (c + TB < e.t1) load(c + TB);
+      const int m = min(TB, e.t1 - c);
+#pragma unroll 1
+      for (int i = 0; i < m; ++i, ot += os) {
+        f32x4 x[NE], y[NE];
+#pragma unroll
+        for (int j = 0; j < NE; ++j) {
+          x[j] = b.k[i][j * L + l];
+          y[j] = b.q[i][j * L + l];
+        }
+        const float r = token(x, y, b.v[i][wrow]);
+        if (l == 0) *ot = (T)r;
+      }
+    }
+  }
+  if (a.update) {
+#pragma unroll
+    for (int j = 0; j < NE; ++j) {
+      f32x4* p = reinterpret_cast<f32x4*>(Sp + j * 4 * L);
+      if (STREAM)
+        __builtin_nontemporal_store(S[j], p);
+      else
+        *p = S[j];
+    }
+  }
+}
+
+template <typename T, int D, bool SINGLE, bool STREAM>
+static hipError_t decay_step_launch(const DecayStepArgs& a, hipStream_t st, Profiler* prof) {
+  prof_begin(prof, "decay_step", st);
+  hipLaunchKernelGGL((decay_step_kernel<T, D, SINGLE, STREAM>),
+                     dim3((unsigned)((size_t)a.b.n_seq * a.Hv * (D / 32))), dim3(STEP_THREADS), 0,
+                     st, a);
+  prof_end(prof, st);
+  return hipGetLastError();
+}
+
+// States of 128 MiB or more in one call go past the caches, as above.
+template <typename T, int D>
+hipError_t launch_decay_step(const DecayStepArgs& a, hipStream_t st, Profiler* prof) {
+  const bool stream = (size_t)a.b.n_seq * a.Hv * D * D * sizeof(float) >= (size_t)128 << 20;
+  if (!a.b.seq_start && a.b.uniform == 1)
+    return stream ? decay_step_launch<T, D, true, true>(a, st, prof)
+                  : decay_step_launch<T, D, true, false>(a, st, prof);
+  return stream ? decay_step_launch<T, D, false, true>(a, st, prof)
+                : decay_step_launch<T, D, false, false>(a, st, prof);
+}
+
+template hipError_t launch_decay_step<bf16, 64>(const DecayStepArgs&, hipStream_t, Profiler*);
+template hipError_t launch_decay_step<bf16, 128>(const DecayStepArgs&, hipStream_t, Profiler*);
+template hipError_t launch_decay_step<float, 64>(const DecayStepArgs&, hipStream_t, Profiler*);
+template hipError_t launch_decay_step<float, 128>(const DecayStepArgs&, hipStream_t, Profiler*);
+
 }  // namespace sfgdn

@@ -8,6 +8,7 @@
 #include <stdint.h>
 #include <stdio.h>
 #include <string>
+#include <type_traits>
 #include <vector>
 
 #include "../../include/sf_gdn.h"
@@ -1162,6 +1163,410 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
     hipError_t e = shape->dtype == SF_DTYPE_BF16 ? launch_residual_norm_bwd<bf16>(a, st, prof)
                                                 : launch_residual_norm_bwd<float>(a, st, prof);
     if (e != hipSuccess) return hip_fail(e, "residual norm launch");
+    return SF_OK;
+  });
+} catch (...) {
+  return host_failure();
+}
+
+}  // extern "C"
+
+// ------------------------------------- linear attention with a decay per head
+namespace {
+
+// Segments of a call.  A scan workgroup takes one item (a segment) of one
+// value head and two share a compute unit, so items of all heads are made
+// about 512, of four blocks at least: shorter ones cost more in boundary
+// states (written, chained and read again) than they give in parallel work.
+constexpr int kDecayGroups = 512, kDecayMinBlocks = 4;
+
+struct DecayCall {
+  DecayArgs a;
+  int D;
+  long long slots;      // boundary states of a head
+  size_t table, bound;  // bytes
+  size_t part;
+};
+
+sf_status make_decay(const sf_decay_shape* p, bool packed, DecayCall& c) {
+  if (!p) return fail(SF_ERR_INVALID_ARG, "shape is NULL");
+  sf_status s;
+  if ((s = check_dtype(p->dtype)) != SF_OK) return s;
+  if (p->n_seq < 0 || p->n_tok < 0) return fail(SF_ERR_INVALID_ARG, "n_seq and n_tok must be >= 0");
+  if (p->Hk <= 0 || p->Hv <= 0 || p->Dk <= 0 || p->Dv <= 0)
+    return fail(SF_ERR_INVALID_ARG, "Hk, Hv, Dk and Dv must be positive");
+  if (p->Hv % p->Hk) return fail(SF_ERR_INVALID_ARG, "Hv must be a multiple of Hk");
+  if (p->Dk != p->Dv || (p->Dk != 64 && p->Dk != 128))
+    return fail(SF_ERR_UNSUPPORTED, "Dk == Dv in {64, 128} supported");
+  if (p->n_tok > (1 << 30)) return fail(SF_ERR_UNSUPPORTED, "n_tok too large");
+  if (p->Hv > (1 << 16) || (long long)p->n_seq * p->Hv > (1LL << 21))
+    return fail(SF_ERR_UNSUPPORTED, "n_seq * Hv too large");
+  if (p->n_seq == 0 && p->n_tok > 0 && !packed)
+    return fail(SF_ERR_INVALID_ARG, "tokens without a sequence");
+  if (!packed && p->n_seq > 0 && p->n_tok % p->n_seq)
+    return fail(SF_ERR_INVALID_ARG, "without seq_start n_tok must be a multiple of n_seq");
+  const int D = p->Dk;
+  c.D = D;
+  DecayArgs& a = c.a;
+  if ((s = token_stride(p->q_stride, (long long)p->Hk * D, "q", &a.qs)) != SF_OK) return s;
+  if ((s = token_stride(p->k_stride, (long long)p->Hk * D, "k", &a.ks)) != SF_OK) return s;
+  if ((s = token_stride(p->v_stride, (long long)p->Hv * D, "v", &a.vs)) != SF_OK) return s;
+  a.n_seq = p->n_seq; a.n_tok = p->n_tok; a.Hv = p->Hv; a.group = p->Hv / p->Hk;
+  a.scale = p->scale;
+  DecayPlan& d = a.plan;
+  d = DecayPlan{};
+  d.T = !packed && p->n_seq > 0 ? p->n_tok / p->n_seq : p->n_tok;
+  const long long blocks = ((long long)p->n_tok + BLK - 1) / BLK * p->Hv;
+  long long L = (blocks + kDecayGroups - 1) / kDecayGroups;
+  if (L < kDecayMinBlocks) L = kDecayMinBlocks;
+  // sequences of one length that fill the GPU by themselves are not cut
+  const long long own = (d.T + BLK - 1) / BLK;
+  if (!packed && ((long long)p->n_seq * p->Hv >= kDecayGroups || L > own)) L = own > 0 ? own : 1;
+  d.L = (int)(L * BLK);
+  if (packed) {
+    c.slots = p->n_tok > 0 ? (p->n_tok - 1) / d.L : 0;
+    d.max_items = p->n_seq + (int)c.slots;
+    d.max_multi = (int)(c.slots < p->n_seq ? c.slots : p->n_seq);
+    d.P = 0;
+    c.table = align_up(sizeof(int) * (kDecayHead + (size_t)d.max_items * kDecayItem +
+                                      (size_t)d.max_multi * kDecayMulti));
+  } else {
+    d.P = d.T > 0 ? (d.T + d.L - 1) / d.L : 1;
+    c.slots = (long long)p->n_seq * (d.P - 1);
+    d.max_items = p->n_seq * d.P;
+    d.max_multi = d.P > 1 ? p->n_seq : 0;
+    c.table = 0;
+  }
+  c.bound = align_up((size_t)c.slots * p->Hv * D * D * 4);
+  c.part = a.group > 1 ? align_up((size_t)p->n_tok * p->Hv * D * 4) : 0;
+  return SF_OK;
+}
+
+size_t decay_ws(const DecayCall& c, bool bwd) {
+  return c.table + (bwd ? 2 * (c.bound + c.part) : c.bound);
+}
+
+// Bytes for either kind of batch: the shape does not say which it is.
+sf_status decay_ws_size(const sf_decay_shape* shape, bool bwd, size_t* bytes) {
+  DecayCall c{};
+  sf_status s = make_decay(shape, true, c);
+  if (s != SF_OK) return s;
+  if (!bytes) return fail(SF_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = decay_ws(c, bwd);
+  if (shape->n_seq > 0 && shape->n_tok % shape->n_seq == 0) {
+    if ((s = make_decay(shape, false, c)) != SF_OK) return s;
+    if (decay_ws(c, bwd) > *bytes) *bytes = decay_ws(c, bwd);
+  }
+  return SF_OK;
+}
+
+sf_status carve_decay(DecayCall& c, bool packed, bool bwd, void* workspace, size_t ws_bytes) {
+  const size_t need = decay_ws(c, bwd);
+  if (need > 0 && (!workspace || ws_bytes < need))
+    return fail(SF_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
+  if (workspace && ((uintptr_t)workspace % kAlign))
+    return fail(SF_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  char* w = (char*)workspace;
+  if (packed) c.a.plan.table = (int*)w;
+  w += c.table;
+  for (int i = 0; i < 1 + bwd; ++i, w += c.bound) c.a.bound[i] = (float*)w;
+  for (int i = 0; bwd && i < 2; ++i, w += c.part) c.a.part[i] = (float*)w;
+  return SF_OK;
+}
+
+sf_status check_floats(const float* p, const char* name) {
+  if ((uintptr_t)p % 4) return fail(SF_ERR_INVALID_ARG, std::string(name) + " is not 4-byte aligned");
+  return SF_OK;
+}
+
+template <typename F> hipError_t by_type(int dtype, int D, F f) {
+  if (dtype == SF_DTYPE_BF16) return D == 64 ? f((bf16)0, std::integral_constant<int, 64>())
+                                             : f((bf16)0, std::integral_constant<int, 128>());
+  return D == 64 ? f(0.f, std::integral_constant<int, 64>())
+                 : f(0.f, std::integral_constant<int, 128>());
+}
+
+}  // namespace
+
+extern "C" {
+
+sf_status sf_gdn_decay_chunk_fwd_workspace_size(const sf_decay_shape* shape, size_t* bytes) try {
+  return decay_ws_size(shape, false, bytes);
+} catch (...) {
+  return host_failure();
+}
+
+sf_status sf_gdn_decay_chunk_bwd_workspace_size(const sf_decay_shape* shape, size_t* bytes) try {
+  return decay_ws_size(shape, true, bytes);
+} catch (...) {
+  return host_failure();
+}
+
+sf_status sf_gdn_decay_chunk_fwd(const sf_decay_shape* shape, const void* q, const void* k,
+                                 const void* v, const float* decay, const int* seq_start,
+                                 const float* S_in, void* o, float* S_out, void* workspace,
+                                 size_t ws_bytes, void* stream) try {
+  DecayCall c{};
+  sf_status s = make_decay(shape, seq_start != nullptr, c);
+  if (s != SF_OK) return s;
+  const sf_decay_shape& p = *shape;
+  DecayArgs& a = c.a;
+  if ((s = check_ints(seq_start, "seq_start")) != SF_OK) return s;
+  if (p.n_seq == 0) return SF_OK;
+  if (!decay) return fail(SF_ERR_INVALID_ARG, "decay is required");
+  if (p.n_tok > 0 && (!q || !k || !v || !o))
+    return fail(SF_ERR_INVALID_ARG, "q, k, v and o are required");
+  const int D = c.D;
+  const size_t es = p.dtype == SF_DTYPE_BF16 ? 2 : 4;
+  const size_t st_n = (size_t)p.n_seq * p.Hv * D * D * 4;
+  std::vector<Range> in = {{q, span(p.n_tok, a.qs, (long long)p.Hk * D, es), "q"},
+                           {k, span(p.n_tok, a.ks, (long long)p.Hk * D, es), "k"},
+                           {v, span(p.n_tok, a.vs, (long long)p.Hv * D, es), "v"},
+                           {S_in, st_n, "S_in"}};
+  std::vector<Range> out = {{o, (size_t)p.n_tok * p.Hv * D * es, "o"},
+                            {S_out, st_n, "S_out"},
+                            {workspace, ws_bytes, "workspace"}};
+  std::vector<Range> small = {{decay, (size_t)p.Hv * 4, "decay"},
+                              {seq_start, ((size_t)p.n_seq + 1) * 4, "seq_start"}};
+  if ((s = check_ptrs(in, out, {})) != SF_OK) return s;
+  if ((s = check_apart(small, out)) != SF_OK) return s;
+  if ((s = check_floats(decay, "decay")) != SF_OK) return s;
+  if ((s = carve_decay(c, seq_start, false, workspace, ws_bytes)) != SF_OK) return s;
+  a.q = q; a.k = k; a.v = v; a.decay = decay; a.seq_start = seq_start; a.S_in = S_in; a.o = o;
+  a.S_out = S_out;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e = by_type(p.dtype, D, [&](auto t, auto d) {
+      return launch_decay_fwd<decltype(t), decltype(d)::value>(a, st, prof);
+    });
+    if (e != hipSuccess) return hip_fail(e, "decay forward launch");
+    return SF_OK;
+  });
+} catch (...) {
+  return host_failure();
+}
+
+sf_status sf_gdn_decay_chunk_bwd(const sf_decay_shape* shape, const void* q, const void* k,
+                                 const void* v, const float* decay, const int* seq_start,
+                                 const float* S_in, const void* dO, const float* dS_out, void* dq,
+                                 void* dk, void* dv, float* dS_in, void* workspace,
+                                 size_t ws_bytes, void* stream) try {
+  DecayCall c{};
+  sf_status s = make_decay(shape, seq_start != nullptr, c);
+  if (s != SF_OK) return s;
+  const sf_decay_shape& p = *shape;
+  DecayArgs& a = c.a;
+  if ((s = check_ints(seq_start, "seq_start")) != SF_OK) return s;
+  if (p.n_seq == 0) return SF_OK;
+  if (!decay) return fail(SF_ERR_INVALID_ARG, "decay is required");
+  if (p.n_tok > 0 && (!q || !k || !v || !dO || !dq || !dk || !dv))
+    return fail(SF_ERR_INVALID_ARG, "q, k, v, dO, dq, dk and dv are required");
+  const int D = c.D;
+  const size_t es = p.dtype == SF_DTYPE_BF16 ? 2 : 4;
+  const size_t st_n = (size_t)p.n_seq * p.Hv * D * D * 4;
+  const size_t nk = (size_t)p.n_tok * p.Hk * D * es, nv = (size_t)p.n_tok * p.Hv * D * es;
+  std::vector<Range> in = {{q, span(p.n_tok, a.qs, (long long)p.Hk * D, es), "q"},
+                           {k, span(p.n_tok, a.ks, (long long)p.Hk * D, es), "k"},
+                           {v, span(p.n_tok, a.vs, (long long)p.Hv * D, es), "v"},
+                           {dO, nv, "dO"}, {S_in, st_n, "S_in"}, {dS_out, st_n, "dS_out"}};
+  std::vector<Range> out = {{dq, nk, "dq"}, {dk, nk, "dk"}, {dv, nv, "dv"}, {dS_in, st_n, "dS_in"},
+                            {workspace, ws_bytes, "workspace"}};
+  std::vector<Range> small = {{decay, (size_t)p.Hv * 4, "decay"},
+                              {seq_start, ((size_t)p.n_seq + 1) * 4, "seq_start"}};
+  if ((s = check_ptrs(in, out, {})) != SF_OK) return s;
+  if ((s = check_apart(small, out)) != SF_OK) return s;
+  if ((s = check_floats(decay, "decay")) != SF_OK) return s;
+  if ((s = carve_decay(c, seq_start, true, workspace, ws_bytes)) != SF_OK) return s;
+  a.q = q; a.k = k; a.v = v; a.decay = decay; a.seq_start = seq_start; a.S_in = S_in; a.dO = dO;
+  a.dS_out = dS_out; a.dq = dq; a.dk = dk; a.dv = dv; a.dS_in = dS_in;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e = by_type(p.dtype, D, [&](auto t, auto d) {
+      return launch_decay_bwd<decltype(t), decltype(d)::value>(a, st, prof);
+    });
+    if (e != hipSuccess) return hip_fail(e, "decay backward launch");
+    return SF_OK;
+  });
+} catch (...) {
+  return host_failure();
+}
+
+sf_status sf_gdn_decay_step(const sf_decay_step_shape* shape, const void* q, const void* k,
+                            const void* v, const float* decay, const int* slots,
+                            const int* seq_start, float* state, void* o, void* stream) try {
+  if (!shape) return fail(SF_ERR_INVALID_ARG, "shape is NULL");
+  const sf_decay_step_shape& p = *shape;
+  sf_status s;
+  DecayStepArgs a{};
+  if ((s = check_dtype(p.dtype)) != SF_OK) return s;
+  if (p.Hk <= 0 || p.Hv <= 0 || p.Dk <= 0 || p.Dv <= 0)
+    return fail(SF_ERR_INVALID_ARG, "Hk, Hv, Dk and Dv must be positive");
+  if (p.Hv % p.Hk) return fail(SF_ERR_INVALID_ARG, "Hv must be a multiple of Hk");
+  if (p.Dk != p.Dv || (p.Dk != 64 && p.Dk != 128))
+    return fail(SF_ERR_UNSUPPORTED, "Dk == Dv in {64, 128} supported");
+  if (p.update != 0 && p.update != 1) return fail(SF_ERR_INVALID_ARG, "update must be 0 or 1");
+  // a workgroup of 256 threads takes 32 rows of a state: at most 2^23 of them,
+  // and a launch holds 2^32 threads
+  if (p.Hv > (1 << 16) || (long long)p.n_seq * p.Hv > (1LL << 21))
+    return fail(SF_ERR_UNSUPPORTED, "n_seq * Hv too large");
+  if ((s = make_batch(p.n_seq, p.n_tok, p.n_slots, p.update, slots, seq_start, a.b)) != SF_OK) return s;
+  const int D = p.Dk;
+  if ((s = token_stride(p.q_stride, (long long)p.Hk * D, "q", &a.qs)) != SF_OK) return s;
+  if ((s = token_stride(p.k_stride, (long long)p.Hk * D, "k", &a.ks)) != SF_OK) return s;
+  if ((s = token_stride(p.v_stride, (long long)p.Hv * D, "v", &a.vs)) != SF_OK) return s;
+  if (p.n_seq == 0 || p.n_tok == 0) return SF_OK;
+  if (!q || !k || !v || !decay || !state || !o)
+    return fail(SF_ERR_INVALID_ARG, "q, k, v, decay, state and o are required");
+  const size_t es = p.dtype == SF_DTYPE_BF16 ? 2 : 4;
+  std::vector<Range> in = {{q, span(p.n_tok, a.qs, (long long)p.Hk * D, es), "q"},
+                           {k, span(p.n_tok, a.ks, (long long)p.Hk * D, es), "k"},
+                           {v, span(p.n_tok, a.vs, (long long)p.Hv * D, es), "v"}};
+  std::vector<Range> out = {{state, (size_t)p.n_slots * p.Hv * D * D * 4, "state"},
+                            {o, (size_t)p.n_tok * p.Hv * D * es, "o"}};
+  std::vector<Range> small = {{decay, (size_t)p.Hv * 4, "decay"},
+                              {slots, (size_t)p.n_seq * 4, "slots"},
+                              {seq_start, ((size_t)p.n_seq + 1) * 4, "seq_start"}};
+  if ((s = check_ptrs(in, out, {})) != SF_OK) return s;
+  if ((s = check_apart(small, out)) != SF_OK) return s;
+  if ((s = check_floats(decay, "decay")) != SF_OK) return s;
+  a.q = q; a.k = k; a.v = v; a.decay = decay; a.state = state; a.o = o;
+  a.Hv = p.Hv; a.group = p.Hv / p.Hk; a.update = p.update; a.scale = p.scale;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e = by_type(p.dtype, D, [&](auto t, auto d) {
+      return launch_decay_step<decltype(t), decltype(d)::value>(a, st, prof);
+    });
+    if (e != hipSuccess) return hip_fail(e, "decay step launch");
+    return SF_OK;
+  });
+} catch (...) {
+  return host_failure();
+}
+
+}  // extern "C"
+
+// --------------------------------------------------- norm and rotation of q, k
+namespace {
+
+sf_status make_rotary(const sf_rotary_shape* p, const int* pos, RotaryArgs& a) {
+  sf_status s;
+  if (!p) return fail(SF_ERR_INVALID_ARG, "shape is NULL");
+  if ((s = check_dtype(p->dtype)) != SF_OK) return s;
+  if (p->N < 0 || p->Hq <= 0 || p->Hk <= 0 || p->D <= 0)
+    return fail(SF_ERR_INVALID_ARG, "Hq, Hk and D must be positive and N >= 0");
+  if (p->D % 8 || p->D > 512)
+    return fail(SF_ERR_UNSUPPORTED, "D must be a multiple of 8, at most 512");
+  if (p->neighbours != 0 && p->neighbours != 1)
+    return fail(SF_ERR_INVALID_ARG, "neighbours must be 0 or 1");
+  if (p->F < 0 || p->F > p->D / 2) return fail(SF_ERR_INVALID_ARG, "F must be in 0 .. D / 2");
+  if (p->F % (p->neighbours ? 4 : 8))
+    return fail(SF_ERR_UNSUPPORTED, "F must be a multiple of 8 (of 4 with neighbours)");
+  if (!(p->eps >= 0.f)) return fail(SF_ERR_INVALID_ARG, "eps must be >= 0");
+  if (!pos && p->N > 0 && p->T <= 0) return fail(SF_ERR_INVALID_ARG, "without pos T must be positive");
+  if (!pos && p->T > 0 && p->first + (p->T - 1) > INT32_MAX)
+    return fail(SF_ERR_UNSUPPORTED, "positions past 2^31 - 1");
+  // heads of a token are counted in 32 bits, and their elements too
+  const long long heads = (long long)p->Hq + p->Hk;
+  if (heads > (1 << 20) || p->N > (1LL << 31) / heads) return fail(SF_ERR_UNSUPPORTED, "N * heads too large");
+  if ((s = token_stride(p->q_stride, (long long)p->Hq * p->D, "q", &a.xs[0])) != SF_OK) return s;
+  if ((s = token_stride(p->k_stride, (long long)p->Hk * p->D, "k", &a.xs[1])) != SF_OK) return s;
+  a.N = p->N; a.T = p->T; a.H[0] = p->Hq; a.H[1] = p->Hk; a.D = p->D; a.F = p->F;
+  a.first = p->first; a.eps = p->eps; a.scale[0] = p->q_scale; a.scale[1] = p->k_scale;
+  a.pos = pos;
+  return SF_OK;
+}
+
+size_t rotary_ws(const RotaryArgs& a, int wanted) {
+  return align_up((size_t)rotary_groups(a.N) * a.D * 4 * wanted);
+}
+
+// The inputs that both directions read.
+sf_status check_rotary(const RotaryArgs& a, size_t es, std::vector<Range> in, std::vector<Range> out) {
+  sf_status s;
+  if (a.F > 0 && !a.freq) return fail(SF_ERR_INVALID_ARG, "freq is required");
+  const char* names[2] = {"q", "k"};
+  const char* wnames[2] = {"wq", "wk"};
+  for (int i = 0; i < 2; ++i) {
+    in.push_back({a.x[i], span(a.N, a.xs[i], (long long)a.H[i] * a.D, es), names[i]});
+    in.push_back({a.w[i], (size_t)a.D * 4, wnames[i]});
+  }
+  if ((s = check_ptrs(in, out, {})) != SF_OK) return s;
+  if ((s = check_apart({{a.pos, (size_t)a.N * 4, "pos"}, {a.freq, (size_t)a.F * 4, "freq"}}, out)) != SF_OK)
+    return s;
+  if ((s = check_ints(a.pos, "pos")) != SF_OK) return s;
+  return check_floats(a.freq, "freq");
+}
+
+}  // namespace
+
+extern "C" {
+
+sf_status sf_gdn_qk_norm_rotary_fwd(const sf_rotary_shape* shape, const void* q, const void* k,
+                                    const int* pos, const float* freq, const float* wq,
+                                    const float* wk, void* yq, void* yk, void* stream) try {
+  RotaryArgs a{};
+  sf_status s = make_rotary(shape, pos, a);
+  if (s != SF_OK) return s;
+  if (a.N == 0) return SF_OK;
+  if (!q || !k || !yq || !yk) return fail(SF_ERR_INVALID_ARG, "q, k, yq and yk are required");
+  a.x[0] = q; a.x[1] = k; a.freq = freq; a.w[0] = wq; a.w[1] = wk; a.y[0] = yq; a.y[1] = yk;
+  const size_t es = es_of(shape->dtype);
+  if ((s = check_rotary(a, es, {},
+                        {{yq, (size_t)a.N * a.H[0] * a.D * es, "yq"},
+                         {yk, (size_t)a.N * a.H[1] * a.D * es, "yk"}})) != SF_OK)
+    return s;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e = shape->dtype == SF_DTYPE_BF16
+                       ? launch_rotary_fwd<bf16>(a, shape->neighbours, st, prof)
+                       : launch_rotary_fwd<float>(a, shape->neighbours, st, prof);
+    if (e != hipSuccess) return hip_fail(e, "rotary launch");
+    return SF_OK;
+  });
+} catch (...) {
+  return host_failure();
+}
+
+sf_status sf_gdn_qk_norm_rotary_bwd_workspace_size(const sf_rotary_shape* shape, size_t* bytes) try {
+  RotaryArgs a{};
+  static const int some = 0;  // the size does not depend on where positions come from
+  sf_status s = make_rotary(shape, &some, a);
+  if (s != SF_OK) return s;
+  if (!bytes) return fail(SF_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = rotary_ws(a, 2);
+  return SF_OK;
+} catch (...) {
+  return host_failure();
+}
+
+sf_status sf_gdn_qk_norm_rotary_bwd(const sf_rotary_shape* shape, const void* q, const void* k,
+                                    const int* pos, const float* freq, const float* wq,
+                                    const float* wk, const void* dyq, const void* dyk, void* dq,
+                                    void* dk, float* dwq, float* dwk, void* workspace,
+                                    size_t ws_bytes, void* stream) try {
+  RotaryArgs a{};
+  sf_status s = make_rotary(shape, pos, a);
+  if (s != SF_OK) return s;
+  if (a.N > 0 && (!q || !k || !dyq || !dyk || !dq || !dk))
+    return fail(SF_ERR_INVALID_ARG, "q, k, dyq, dyk, dq and dk are required");
+  if ((dwq && !wq) || (dwk && !wk)) return fail(SF_ERR_INVALID_ARG, "a weight's gradient needs the weight");
+  a.x[0] = q; a.x[1] = k; a.freq = freq; a.w[0] = wq; a.w[1] = wk; a.dy[0] = dyq; a.dy[1] = dyk;
+  a.y[0] = dq; a.y[1] = dk; a.dw[0] = dwq; a.dw[1] = dwk;
+  const size_t es = es_of(shape->dtype), vec = (size_t)a.D * 4;
+  const size_t nq = (size_t)a.N * a.H[0] * a.D * es, nk = (size_t)a.N * a.H[1] * a.D * es;
+  if ((s = check_rotary(a, es, {{dyq, nq, "dyq"}, {dyk, nk, "dyk"}},
+                        {{dq, nq, "dq"}, {dk, nk, "dk"}, {dwq, vec, "dwq"}, {dwk, vec, "dwk"},
+                         {workspace, ws_bytes, "workspace"}})) != SF_OK)
+    return s;
+  const int wanted = (dwq ? 1 : 0) + (dwk ? 1 : 0);
+  if ((s = check_norm_ws(rotary_ws(a, wanted), workspace, ws_bytes)) != SF_OK) return s;
+  a.part = (float*)workspace;
+  hipStream_t st = (hipStream_t)stream;
+  return run_locked([&](Profiler* prof) -> sf_status {
+    hipError_t e = shape->dtype == SF_DTYPE_BF16
+                       ? launch_rotary_bwd<bf16>(a, shape->neighbours, st, prof)
+                       : launch_rotary_bwd<float>(a, shape->neighbours, st, prof);
+    if (e != hipSuccess) return hip_fail(e, "rotary launch");
     return SF_OK;
   });
 } catch (...) {

@@ -14,6 +14,7 @@
 #include <c10/core/DeviceGuard.h>
 
 #include <string>
+#include <vector>
 
 #include "../../include/sf_gdn.h"
 
@@ -32,6 +33,14 @@ struct Entries {
   decltype(&sf_gdn_residual_norm_fwd) residual_norm_fwd;
   decltype(&sf_gdn_residual_norm_bwd) residual_norm_bwd;
   decltype(&sf_gdn_residual_norm_bwd_workspace_size) residual_norm_bwd_workspace_size;
+  decltype(&sf_gdn_decay_chunk_fwd) decay_chunk_fwd;
+  decltype(&sf_gdn_decay_chunk_fwd_workspace_size) decay_chunk_fwd_workspace_size;
+  decltype(&sf_gdn_decay_chunk_bwd) decay_chunk_bwd;
+  decltype(&sf_gdn_decay_chunk_bwd_workspace_size) decay_chunk_bwd_workspace_size;
+  decltype(&sf_gdn_decay_step) decay_step;
+  decltype(&sf_gdn_qk_norm_rotary_fwd) qk_norm_rotary_fwd;
+  decltype(&sf_gdn_qk_norm_rotary_bwd) qk_norm_rotary_bwd;
+  decltype(&sf_gdn_qk_norm_rotary_bwd_workspace_size) qk_norm_rotary_bwd_workspace_size;
 } g_abi;
 PyObject* g_fail = nullptr;  // fail(status, call): raises the package's error
 
@@ -545,6 +554,295 @@ PyObject* residual_norm_bwd(const Args& a) {
   return tuple({&dx, &dr, &dw, &ds, &ws});
 }
 
+// The decay chunk's shape from q, k [B, T, Hk, D], v [B, T, Hv, D], or from
+// packed rows [n_tok, H, D] with seq_start (without it: one sequence).
+struct DecayChunk {
+  sf_decay_shape s{};
+  int64_t n_seq, Hv, Dv, Dk;
+};
+DecayChunk decay_chunk(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& decay,
+                       const Tensor* seq_start, double scale, c10::Device dev) {
+  DecayChunk c;
+  const ScalarType dt = q.scalar_type();
+  c.s.dtype = dtype_code(q, "q");
+  if ((q.dim() != 3 && q.dim() != 4) || v.dim() != q.dim())
+    value_error("q and v must be [B, T, heads, D], or [n_tok, heads, D] packed");
+  if (seq_start && q.dim() != 3) value_error("packed sequences (seq_start) are [n_tok, heads, D]");
+  c.Dk = q.size(-1);
+  c.Dv = v.size(-1);
+  c.Hv = v.size(-2);
+  const int64_t Hk = q.size(-2);
+  std::vector<int64_t> want(q.sizes().begin(), q.sizes().end());
+  need_type(k, "k", dt, want, dev);
+  want[want.size() - 2] = c.Hv;
+  want.back() = c.Dv;
+  need_type(v, "v", dt, want, dev);
+  need(decay, "decay", ScalarType::Float, {c.Hv}, dev);
+  c.s.q_stride = token_rows(q, "q", 2);
+  c.s.k_stride = token_rows(k, "k", 2);
+  c.s.v_stride = token_rows(v, "v", 2);
+  int64_t n_tok = q.size(0);
+  if (q.dim() == 4) {
+    c.n_seq = q.size(0);
+    if (q.size(1) && c.n_seq > INT_MAX / q.size(1)) value_error("n_tok is too large");
+    n_tok *= q.size(1);
+  } else {
+    c.n_seq = seq_start ? batch(nullptr, seq_start, 0, dev) : 1;
+  }
+  c.s.n_seq = fits(c.n_seq, "n_seq");
+  c.s.n_tok = fits(n_tok, "n_tok");
+  c.s.Hk = fits(Hk, "Hk");
+  c.s.Hv = fits(c.Hv, "Hv");
+  c.s.Dk = fits(c.Dk, "Dk");
+  c.s.Dv = fits(c.Dv, "Dv");
+  c.s.scale = (float)scale;
+  return c;
+}
+
+// q, k, v, decay, S_in, seq_start, scale, o, S_out, workspace, stream -> o, S_out, workspace
+PyObject* decay_chunk_fwd(const Args& a) {
+  a.count(11);
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
+               &decay = tensor(a[3], "decay");
+  const Tensor *S_in = optional(a[4], "S_in"), *seq_start = optional(a[5], "seq_start"),
+               *o = optional(a[7], "o"), *S_out = optional(a[8], "S_out"),
+               *given = optional(a[9], "workspace");
+  const c10::Device dev = device_of(q, "q");
+  const DecayChunk c = decay_chunk(q, k, v, decay, seq_start, a.real(6), dev);
+  void* st = a.stream(10);
+  need(S_in, "S_in", ScalarType::Float, {c.n_seq, c.Hv, c.Dv, c.Dk}, dev);
+  need(o, "o", q.scalar_type(), v.sizes(), dev);
+  need(S_out, "S_out", ScalarType::Float, {c.n_seq, c.Hv, c.Dv, c.Dk}, dev);
+  const Tensor made_o = o ? Tensor() : new_like(v, v.sizes());
+  const Tensor made_S = S_out ? Tensor() : at::empty({c.n_seq, c.Hv, c.Dv, c.Dk},
+                                                     v.options().dtype(ScalarType::Float));
+  if (!o) o = &made_o;
+  if (!S_out) S_out = &made_S;
+  size_t bytes = 0;
+  run(dev, "sf_gdn_decay_chunk_fwd_workspace_size",
+      [&] { return g_abi.decay_chunk_fwd_workspace_size(&c.s, &bytes); });
+  const Tensor ws = workspace(given, bytes, q);
+  run(dev, "sf_gdn_decay_chunk_fwd", [&] {
+    return g_abi.decay_chunk_fwd(&c.s, ptr(q), ptr(k), ptr(v), f32(&decay), i32(seq_start), f32(S_in),
+                                 out(o), (float*)out(S_out), ws.defined() ? ws.data_ptr() : nullptr,
+                                 bytes_of(ws), st);
+  });
+  written({o, S_out, &ws});
+  return tuple({o, S_out, &ws});
+}
+
+// q, k, v, decay, S_in, dO, dS_out, seq_start, scale, grads, want_dS_in, workspace, stream
+//   -> dq, dk, dv, dS_in, workspace
+PyObject* decay_chunk_bwd(const Args& a) {
+  a.count(13);
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
+               &decay = tensor(a[3], "decay"), &dO = tensor(a[5], "dO");
+  const Tensor *S_in = optional(a[4], "S_in"), *dS_out = optional(a[6], "dS_out"),
+               *seq_start = optional(a[7], "seq_start"), *given = optional(a[11], "workspace");
+  const c10::Device dev = device_of(q, "q");
+  const DecayChunk c = decay_chunk(q, k, v, decay, seq_start, a.real(8), dev);
+  const ScalarType dt = q.scalar_type();
+  const std::vector<int64_t> state{c.n_seq, c.Hv, c.Dv, c.Dk};
+  void* st = a.stream(12);
+  need(S_in, "S_in", ScalarType::Float, state, dev);
+  need(dO, "dO", dt, v.sizes(), dev);
+  need(dS_out, "dS_out", ScalarType::Float, state, dev);
+  const bool want = a.truth(10);
+  PyObject* g[4];
+  unpack(a[9], 4, g);
+  Tensor dq, dk, dv, dS;
+  if (a[9] == Py_None) {
+    dq = new_like(q, q.sizes());
+    dk = new_like(k, k.sizes());
+    dv = new_like(v, v.sizes());
+    if (want) dS = at::empty(state, v.options().dtype(ScalarType::Float));
+  } else {
+    dq = tensor(g[0], "dq");
+    need(dq, "dq", dt, q.sizes(), dev);
+    dk = tensor(g[1], "dk");
+    need(dk, "dk", dt, k.sizes(), dev);
+    dv = tensor(g[2], "dv");
+    need(dv, "dv", dt, v.sizes(), dev);
+    if (want) {
+      dS = tensor(g[3], "dS_in");
+      need(dS, "dS_in", ScalarType::Float, state, dev);
+    }
+  }
+  size_t bytes = 0;
+  run(dev, "sf_gdn_decay_chunk_bwd_workspace_size",
+      [&] { return g_abi.decay_chunk_bwd_workspace_size(&c.s, &bytes); });
+  const Tensor ws = workspace(given, bytes, q);
+  run(dev, "sf_gdn_decay_chunk_bwd", [&] {
+    return g_abi.decay_chunk_bwd(&c.s, ptr(q), ptr(k), ptr(v), f32(&decay), i32(seq_start), f32(S_in),
+                                 ptr(dO), f32(dS_out), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                 dS.defined() ? (float*)dS.data_ptr() : nullptr,
+                                 ws.defined() ? ws.data_ptr() : nullptr, bytes_of(ws), st);
+  });
+  written({&dq, &dk, &dv, &dS, &ws});
+  return tuple({&dq, &dk, &dv, &dS, &ws});
+}
+
+// q, k, v, decay, state, slots, seq_start, o, update, scale, stream -> o
+PyObject* decay_step(const Args& a) {
+  a.count(11);
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
+               &decay = tensor(a[3], "decay"), &state = tensor(a[4], "state");
+  const Tensor *slots = optional(a[5], "slots"), *seq_start = optional(a[6], "seq_start"),
+               *o = optional(a[7], "o");
+  const c10::Device dev = device_of(q, "q");
+  const ScalarType dt = q.scalar_type();
+  sf_decay_step_shape s{};
+  s.dtype = dtype_code(q, "q");
+  if (q.dim() != 3 || v.dim() != 3 || state.dim() != 4)
+    value_error("q and v must be [n_tok, heads, D], state [n_slots, Hv, Dv, Dk]");
+  const int64_t N = q.size(0), Hk = q.size(1), Dk = q.size(2), Hv = v.size(1), Dv = v.size(2),
+                slots_n = state.size(0);
+  need_type(k, "k", dt, {N, Hk, Dk}, dev);
+  need_type(v, "v", dt, {N, Hv, Dv}, dev);
+  s.q_stride = token_rows(q, "q", 2);
+  s.k_stride = token_rows(k, "k", 2);
+  s.v_stride = token_rows(v, "v", 2);
+  need(decay, "decay", ScalarType::Float, {Hv}, dev);
+  need(state, "state", ScalarType::Float, {slots_n, Hv, Dv, Dk}, dev);
+  s.n_seq = batch(slots, seq_start, slots_n, dev);
+  s.n_tok = fits(N, "n_tok");
+  s.n_slots = fits(slots_n, "n_slots");
+  s.Hk = fits(Hk, "Hk");
+  s.Hv = fits(Hv, "Hv");
+  s.Dk = fits(Dk, "Dk");
+  s.Dv = fits(Dv, "Dv");
+  s.update = a.truth(8);
+  s.scale = a.real(9);
+  void* st = a.stream(10);
+  need(o, "o", dt, {N, Hv, Dv}, dev);
+  const Tensor made = o ? Tensor() : new_like(v, {N, Hv, Dv});
+  if (!o) o = &made;
+  run(dev, "sf_gdn_decay_step", [&] {
+    return g_abi.decay_step(&s, ptr(q), ptr(k), ptr(v), f32(&decay), i32(slots), i32(seq_start),
+                            (float*)out(&state), out(o), st);
+  });
+  written({s.update ? &state : nullptr, o});
+  return wrap(o);
+}
+
+// The rotary call's shape from q [..., Hq, D], k [..., Hk, D].
+sf_rotary_shape rotary_shape(const Tensor& q, const Tensor& k, const Tensor* pos, const Tensor* freq,
+                             const Tensor* wq, const Tensor* wk, c10::Device dev) {
+  if (q.dim() < 3 || k.dim() != q.dim())
+    value_error("q and k must be [..., heads, D], got shapes " + text(q.sizes()) + " and " + text(k.sizes()));
+  sf_rotary_shape s{};
+  const int64_t D = q.size(-1), Hq = q.size(-2), Hk = k.size(-2);
+  s.dtype = dtype_code(q, "q");
+  std::vector<int64_t> want(q.sizes().begin(), q.sizes().end());
+  want[want.size() - 2] = Hk;
+  need_type(k, "k", q.scalar_type(), want, dev);
+  s.N = 1;
+  for (int64_t d = 0; d < q.dim() - 2; ++d) s.N *= q.size(d);
+  s.T = q.size(-3);
+  s.Hq = fits(Hq, "Hq");
+  s.Hk = fits(Hk, "Hk");
+  s.D = fits(D, "D");
+  s.q_stride = token_rows(q, "q", 2);
+  s.k_stride = token_rows(k, "k", 2);
+  want.resize(want.size() - 2);
+  need(pos, "pos", ScalarType::Int, want, dev);
+  if (freq) {
+    if (freq->dim() != 1) value_error("freq must have one dimension");
+    s.F = fits(freq->size(0), "F");
+    need(*freq, "freq", ScalarType::Float, {freq->size(0)}, dev);
+  }
+  need(wq, "wq", ScalarType::Float, {D}, dev);
+  need(wk, "wk", ScalarType::Float, {D}, dev);
+  return s;
+}
+
+// q, k, pos, freq, wq, wk, eps, q_scale, k_scale, neighbours, first, yq, yk, stream -> yq, yk
+PyObject* qk_norm_rotary_fwd(const Args& a) {
+  a.count(14);
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+  const Tensor *pos = optional(a[2], "pos"), *freq = optional(a[3], "freq"), *wq = optional(a[4], "wq"),
+               *wk = optional(a[5], "wk"), *yq = optional(a[11], "yq"), *yk = optional(a[12], "yk");
+  const c10::Device dev = device_of(q, "q");
+  sf_rotary_shape s = rotary_shape(q, k, pos, freq, wq, wk, dev);
+  s.eps = a.real(6);
+  s.q_scale = a.real(7);
+  s.k_scale = a.real(8);
+  s.neighbours = a.truth(9);
+  s.first = a.small(10);
+  void* st = a.stream(13);
+  need(yq, "yq", q.scalar_type(), q.sizes(), dev);
+  need(yk, "yk", q.scalar_type(), k.sizes(), dev);
+  const Tensor made_q = yq ? Tensor() : new_like(q, q.sizes());
+  const Tensor made_k = yk ? Tensor() : new_like(k, k.sizes());
+  if (!yq) yq = &made_q;
+  if (!yk) yk = &made_k;
+  run(dev, "sf_gdn_qk_norm_rotary_fwd", [&] {
+    return g_abi.qk_norm_rotary_fwd(&s, ptr(q), ptr(k), i32(pos), f32(freq), f32(wq), f32(wk), out(yq),
+                                    out(yk), st);
+  });
+  written({yq, yk});
+  return tuple({yq, yk});
+}
+
+// q, k, pos, freq, wq, wk, dyq, dyk, eps, q_scale, k_scale, neighbours, first, grads, want_dw,
+// workspace, stream -> dq, dk, dwq, dwk, workspace
+PyObject* qk_norm_rotary_bwd(const Args& a) {
+  a.count(17);
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &dyq = tensor(a[6], "dyq"),
+               &dyk = tensor(a[7], "dyk");
+  const Tensor *pos = optional(a[2], "pos"), *freq = optional(a[3], "freq"), *wq = optional(a[4], "wq"),
+               *wk = optional(a[5], "wk"), *given = optional(a[15], "workspace");
+  const c10::Device dev = device_of(q, "q");
+  const ScalarType dt = q.scalar_type();
+  sf_rotary_shape s = rotary_shape(q, k, pos, freq, wq, wk, dev);
+  s.eps = a.real(8);
+  s.q_scale = a.real(9);
+  s.k_scale = a.real(10);
+  s.neighbours = a.truth(11);
+  s.first = a.small(12);
+  void* st = a.stream(16);
+  need(dyq, "dyq", dt, q.sizes(), dev);
+  need(dyk, "dyk", dt, k.sizes(), dev);
+  const bool want_dw = a.truth(14);
+  PyObject* g[4];
+  unpack(a[13], 4, g);
+  Tensor dq, dk, dwq, dwk, ws;
+  if (a[13] == Py_None) {
+    dq = new_like(q, q.sizes());
+    dk = new_like(k, k.sizes());
+    if (want_dw && wq) dwq = new_f32(q, s.D);
+    if (want_dw && wk) dwk = new_f32(q, s.D);
+  } else {
+    dq = tensor(g[0], "dq");
+    need(dq, "dq", dt, q.sizes(), dev);
+    dk = tensor(g[1], "dk");
+    need(dk, "dk", dt, k.sizes(), dev);
+    if (want_dw && wq) {
+      dwq = tensor(g[2], "dwq");
+      need(dwq, "dwq", ScalarType::Float, {s.D}, dev);
+    }
+    if (want_dw && wk) {
+      dwk = tensor(g[3], "dwk");
+      need(dwk, "dwk", ScalarType::Float, {s.D}, dev);
+    }
+  }
+  if (dwq.defined() || dwk.defined()) {
+    size_t bytes = 0;
+    run(dev, "sf_gdn_qk_norm_rotary_bwd_workspace_size",
+        [&] { return g_abi.qk_norm_rotary_bwd_workspace_size(&s, &bytes); });
+    ws = workspace(given, bytes, q);
+  }
+  run(dev, "sf_gdn_qk_norm_rotary_bwd", [&] {
+    return g_abi.qk_norm_rotary_bwd(&s, ptr(q), ptr(k), i32(pos), f32(freq), f32(wq), f32(wk),
+                                    ptr(dyq), ptr(dyk), dq.data_ptr(), dk.data_ptr(),
+                                    dwq.defined() ? (float*)dwq.data_ptr() : nullptr,
+                                    dwk.defined() ? (float*)dwk.data_ptr() : nullptr,
+                                    ws.defined() ? ws.data_ptr() : nullptr, bytes_of(ws), st);
+  });
+  written({&dq, &dk, &dwq, &dwk, &ws});
+  return tuple({&dq, &dk, &dwq, &dwk, &ws});
+}
+
 // bind(fail, addresses of the entry points in the order of Entries)
 PyObject* bind(const Args& a) {
   constexpr Py_ssize_t n = sizeof(Entries) / sizeof(void*);
@@ -561,7 +859,9 @@ PyObject* bind(const Args& a) {
 #define CALL(f) {#f, (PyCFunction)(void (*)(void))entry<f>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {CALL(bind),           CALL(recurrent_step),    CALL(shortconv_step),
                          CALL(gated_norm_fwd), CALL(gated_norm_bwd),    CALL(residual_norm_fwd),
-                         CALL(residual_norm_bwd), {nullptr, nullptr, 0, nullptr}};
+                         CALL(residual_norm_bwd), CALL(decay_chunk_fwd), CALL(decay_chunk_bwd),
+                         CALL(decay_step), CALL(qk_norm_rotary_fwd), CALL(qk_norm_rotary_bwd),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods};
 
 }  // namespace
