@@ -27,9 +27,6 @@
 
 namespace sfgdn {
 
-constexpr int DECAY_NW = 4;  // waves per workgroup
-constexpr int DECAY_NT = 64 * DECAY_NW;
-
 // One item: a segment of a sequence.  prev, next: the boundary slots before
 // and after it (-1 at the sequence's ends).
 struct DecayItem {
@@ -54,15 +51,16 @@ __device__ __forceinline__ bool decay_item(const DecayPlan& p, int i, DecayItem&
 
 // a^e for e >= 0, by squaring in 64 bits: exact to a rounding for every a,
 // 0 and values near 1 among them.
-__device__ __forceinline__ float decay_pow(float a, int e) {
+__device__ __forceinline__ double decay_pow64(float a, int e) {
   double r = 1.0, b = a;
   while (e > 0) {
     if (e & 1) r *= b;
     b *= b;
     e >>= 1;
   }
-  return (float)r;
+  return r;
 }
+__device__ __forceinline__ float decay_pow(float a, int e) { return (float)decay_pow64(a, e); }
 
 // ------------------------------------------------------------------ the plan
 // Items and boundary slots of packed sequences, by one workgroup.  Offsets are
@@ -138,121 +136,305 @@ __global__ __launch_bounds__(1024) void decay_plan_kernel(const int* seq_start, 
 }
 
 // --------------------------------------------------------------------- tiles
-// Operands are bf16: one plane for bf16 tensors; two for fp32 ones, x = hi +
-// lo, with the three products hi hi + hi lo + lo hi summed in fp32 (what is
-// left out is below 2^-16 of a term, and about 2e-6 of a sum; fp32 matrix
-// instructions would take five times the time of the three).
-template <typename T> constexpr int planes() { return sizeof(T) == 2 ? 1 : 2; }
+// Operands are bf16 planes: a bf16 tensor is one, an fp32 tensor three, x = x0
+// + x1 + x2 with what each plane leaves of the one before (24 bits).  Products
+// run over the pairs of planes down to 2^-16 of the first, summed in fp32, the
+// smallest first: six for two fp32 tensors, whose results differ from exact
+// products of fp32 by less than the sums do (fp32 matrix instructions have a
+// sixteenth of the rate).
+template <typename T> struct DecayKind;
+template <> struct DecayKind<bf16> {
+  static constexpr int C = 64;  // tokens of a block
+  static constexpr int NP = 1;  // planes of a tensor
+  static constexpr int NY = 1;  // planes of P and of the state's copy, on the way to bf16 outputs
+};
+template <> struct DecayKind<float> {
+  static constexpr int C = 32;
+  static constexpr int NP = 3;
+  static constexpr int NY = 3;
+};
+constexpr int DECAY_NS = 3;  // planes of w times its decay on the way to the fp32 state
 
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mma_planes(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 c) {
-  if constexpr (NA == 2) c = Mma<bf16>::mma(a[1], b[0], c);
-  if constexpr (NB == 2) c = Mma<bf16>::mma(a[0], b[1], c);
-  return Mma<bf16>::mma(a[0], b[0], c);
+  constexpr int N = NA > NB ? NA : NB;
+#pragma unroll
+  for (int n = N - 1; n >= 0; --n)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (n - i >= 0 && n - i < NB) c = Mma<bf16>::mma(a[i], b[n - i], c);
+  return c;
 }
 
-// Rows of D values, in planes of 64 x D bf16 (swizzled).
-template <typename T, int D> struct DecayTile {
-  static constexpr int NP = planes<T>();
-  static constexpr int ELEMS = BLK * D;  // of a plane
-  static constexpr int VEC = 16 / (int)sizeof(T), CPR = D / VEC, NCH = BLK * CPR / DECAY_NT;
+// acc(i, j) += a[i] b[j] over all tiles, pair of planes by pair of planes, so
+// that as many products as there are tiles lie between two into one of them.
+template <int M, int N, int NA, int NB, typename F>
+__device__ __forceinline__ void mma_grid(const bf16x8 (&a)[M][NA], const bf16x8 (&b)[N][NB], F acc) {
+  constexpr int K = NA > NB ? NA : NB;
+#pragma unroll
+  for (int n = K - 1; n >= 0; --n)
+#pragma unroll
+    for (int p = 0; p < NA; ++p)
+      if (n - p >= 0 && n - p < NB)
+#pragma unroll
+        for (int i = 0; i < M; ++i)
+#pragma unroll
+          for (int j = 0; j < N; ++j) acc(i, j) = Mma<bf16>::mma(a[i][p], b[j][n - p], acc(i, j));
+}
 
-  __device__ static __forceinline__ void load(uint4 (&r)[NCH], const T* g, size_t row_stride,
-                                              int nvalid) {
+// N values to planes, a pair at a time.
+typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+template <int N, int K, typename V>
+__device__ __forceinline__ void to_planes(const float (&x)[N], V (&f)[K]) {
 #pragma unroll
-    for (int it = 0; it < NCH; ++it) {
-      const int c = threadIdx.x + DECAY_NT * it;
-      const int row = min(c / CPR, nvalid - 1), ch = c % CPR;
-      r[it] = *reinterpret_cast<const uint4*>(g + (size_t)row * row_stride + ch * VEC);
-    }
-  }
-  __device__ static __forceinline__ void to_lds(const uint4 (&r)[NCH], bf16* s, int nvalid) {
+  for (int j = 0; j < N; j += 2) {
+    float a = x[j], b = x[j + 1];
 #pragma unroll
-    for (int it = 0; it < NCH; ++it) {
-      const int c = threadIdx.x + DECAY_NT * it;
-      const int row = c / CPR, ch = c % CPR;
-      const bool ok = row < nvalid;
-      uint4 v = r[it];
-      v.x = ok ? v.x : 0u;
-      v.y = ok ? v.y : 0u;
-      v.z = ok ? v.z : 0u;
-      v.w = ok ? v.w : 0u;
-      bf16* p = lds_sw(s + row * D + ch * VEC, D);
-      if constexpr (NP == 1) {
-        *reinterpret_cast<uint4*>(p) = v;
-      } else {
-        const f32x4 f = __builtin_bit_cast(f32x4, v);
-        bf16x4 hi, lo;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          hi[e] = (bf16)f[e];
-          lo[e] = (bf16)(f[e] - (float)hi[e]);
-        }
-        *reinterpret_cast<bf16x4*>(p) = hi;
-        *reinterpret_cast<bf16x4*>(p + ELEMS) = lo;
+    for (int p = 0; p < K; ++p) {
+      const bf16x2 h = __builtin_convertvector((f32x2{a, b}), bf16x2);
+      f[p][j] = h[0];
+      f[p][j + 1] = h[1];
+      if (p + 1 < K) {
+        const unsigned u = __builtin_bit_cast(unsigned, h);
+        a -= __uint_as_float(u << 16);
+        b -= __uint_as_float(u & 0xffff0000u);
       }
     }
   }
-  // operand rows from row0, contraction along the row
-  template <int KO>
-  __device__ static __forceinline__ void rows(const bf16* s, int row0, int step, bf16x8 (&f)[NP]) {
+}
+
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+template <typename V> __device__ __forceinline__ auto lds_at(unsigned at) {
+  typedef __attribute__((address_space(3))) V lds_t;
+  return (lds_t*)(size_t)at;
+}
+// 16-byte units of a lane's transpose read (see ds_tr4)
+__device__ __forceinline__ bf16x4 lds_tr4(unsigned at) {
+  return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_at<i16x4>(at)));
+}
+
+// Waves of a workgroup.
+template <int D> constexpr int decay_waves() { return 4; }
+
+// A block's rows of D values in LDS, in planes of C x D bf16, each row's
+// 16-byte units permuted as by lds_sw.
+template <typename T, int D> struct DecayTile {
+  static constexpr int C = DecayKind<T>::C, NP = DecayKind<T>::NP, NT = 64 * decay_waves<D>();
+  static constexpr int RB = 2 * D, BYTES = C * RB;  // of a plane's row, of a plane
+  static constexpr int NW16 = sizeof(T) / 2;        // 16-byte loads for 16 bytes of a plane
+  static constexpr int VEC = 16 / (int)sizeof(T), CPR = D / VEC, RPT = NT / CPR, NCH = C / RPT;
+  static constexpr __host__ __device__ int swizzle(int row) {
+    return D == 128 ? row & 15 : (row >> 1) & 7;
+  }
+  static_assert(C % RPT == 0, "a tile splits evenly over the workgroup");
+
+  // A thread's first piece of a tile and the bytes to its next ones.
+  struct Rows {
+    unsigned at, step;
+    __device__ __forceinline__ Rows(long long stride) {
+      at = (unsigned)((threadIdx.x / CPR * stride + threadIdx.x % CPR * VEC) * sizeof(T));
+      step = (unsigned)(RPT * stride * sizeof(T));
+    }
+  };
+  // Rows 0 .. nv-1 of a block: past them a load gives zeros and a store is
+  // dropped.  (A block spans less than 2^31 bytes: the strides are checked.)
+  __device__ static __forceinline__ __amdgpu_buffer_rsrc_t block(const T* g, long long stride, int nv) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(g), 0,
+                                             (int)(((nv - 1) * stride + D) * sizeof(T)), 0x00020000);
+  }
+  __device__ static __forceinline__ void load(u32x4 (&r)[NCH], const Rows& o, __amdgpu_buffer_rsrc_t g) {
+#pragma unroll
+    for (int it = 0; it < NCH; ++it)
+      r[it] = __builtin_bit_cast(
+          u32x4, __builtin_amdgcn_raw_buffer_load_b128(g, (int)(o.at + it * o.step), 0, 0));
+  }
+  // at: the tile's LDS address
+  __device__ static __forceinline__ unsigned piece(unsigned at) {
+    const int row = threadIdx.x / CPR, b = threadIdx.x % CPR * 16 / NW16;  // byte in a plane's row
+    return at + row * RB + ((b & ~15) ^ (swizzle(row) << 4)) + (b & 15);
+  }
+  static __device__ __forceinline__ unsigned piece_of(unsigned p, int it) {
+    static_assert(RPT >= 8 && (RPT & (RPT - 1)) == 0, "row + RPT it: bits of their own");
+    return (p ^ swizzle(RPT * it) << 4) + it * RPT * RB;
+  }
+  __device__ static __forceinline__ void to_lds(const u32x4 (&r)[NCH], unsigned at) {
+    const unsigned p = piece(at);
+#pragma unroll
+    for (int it = 0; it < NCH; ++it) {
+      const unsigned q = piece_of(p, it);
+      if constexpr (NP == 1) {
+        *lds_at<u32x4>(q) = r[it];
+      } else {
+        const f32x4 f = __builtin_bit_cast(f32x4, r[it]);
+        const float x[4] = {f[0], f[1], f[2], f[3]};
+        bf16x4 h[NP];
+        to_planes(x, h);
+#pragma unroll
+        for (int i = 0; i < NP; ++i) *lds_at<bf16x4>(q + i * BYTES) = h[i];
+      }
+    }
+  }
+  // The tile's first plane to a block's rows, each thread the pieces that it
+  // writes itself in to_lds (so that needs no barrier after this).
+  __device__ static __forceinline__ void rows_out(const Rows& o, __amdgpu_buffer_rsrc_t g, unsigned at) {
+    const unsigned p = piece(at);
+#pragma unroll
+    for (int it = 0; it < NCH; ++it)
+      __builtin_amdgcn_raw_buffer_store_b128(*lds_at<u32x4>(piece_of(p, it)), g,
+                                             (int)(o.at + it * o.step), 0, 0);
+  }
+  // Operand reads.  The swizzle changes address bits that a lane's row decides,
+  // the same for every tile of 16 rows, so a lane has one base for each form
+  // of read and the rest is a constant to XOR and one to add (which the read
+  // takes as its offset): without that, some hundred addresses would each
+  // want a register.
+  struct Lane {
+    unsigned std, perm, col;
+    __device__ __forceinline__ Lane() {
+      const int l = lane_id(), g = l >> 4, i = l & 15, r = 8 * g + (i >> 2);
+      std = i * RB + ((g ^ swizzle(i)) << 4);
+      perm = i * RB + (((g >> 1) ^ swizzle(i)) << 4) + 8 * (g & 1);
+      col = r * RB + (((i >> 1 & 1) ^ swizzle(r)) << 4) + 8 * (i & 1);
+    }
+    // not kept in registers per use over the blocks
+    __device__ __forceinline__ void fresh() {
+      __asm__ volatile("" : "+v"(std), "+v"(perm), "+v"(col));
+    }
+  };
+  // operand rows from row0 (a multiple of 16), contraction along the row
+  __device__ static __forceinline__ void rows_std(const Lane& l, unsigned at, int row0, int step,
+                                                  bf16x8 (&f)[NP]) {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
-      f[p] = frag_row<bf16, KO>(s + p * ELEMS + row0 * D, D, step);
+      f[p] = *lds_at<bf16x8>((l.std ^ step << 6) + (at + p * BYTES + row0 * RB));
   }
-  // operand rows = columns from col0, contraction along the tokens
-  __device__ static __forceinline__ void cols(const bf16* s, int col0, int step, bf16x8 (&f)[NP]) {
+  __device__ static __forceinline__ void rows_perm(const Lane& l, unsigned at, int row0, int step,
+                                                   bf16x8 (&f)[NP]) {
 #pragma unroll
-    for (int p = 0; p < NP; ++p) f[p] = frag_tr<bf16, STD>(s + p * ELEMS + col0, D, step);
+    for (int p = 0; p < NP; ++p) {
+      const unsigned o = at + p * BYTES + row0 * RB;
+      const bf16x4 lo = *lds_at<bf16x4>((l.perm ^ step << 6) + o);
+      const bf16x4 hi = *lds_at<bf16x4>((l.perm ^ step << 6 ^ 32) + o);
+      f[p] = bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
+  }
+  // operand rows = columns 16 c .., contraction along the tokens
+  __device__ static __forceinline__ void cols(const Lane& l, unsigned at, int c, int step,
+                                              bf16x8 (&f)[NP]) {
+#pragma unroll
+    for (int p = 0; p < NP; ++p) {
+      const unsigned o = at + p * BYTES + 32 * step * RB;
+      const bf16x4 lo = lds_tr4((l.col ^ c << 5) + o);
+      const bf16x4 hi = lds_tr4((l.col ^ c << 5 ^ swizzle(4) << 4) + (o + 4 * RB));
+      f[p] = bf16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
   }
 };
 
-// Eight values to bf16 planes.
-__device__ __forceinline__ void to_planes(const float (&x)[8], bf16x8 (&f)[1]) {
+// P: rows r of C bf16, in planes.
+template <int C> struct DecayP {
+  static constexpr int RB = 2 * C, BYTES = C * RB;
+  static_assert(C == 64 || C == 32, "rows of 128 bytes are swizzled, rows of 64 lie as they are");
+  struct Lane {
+    unsigned w, r;
+    __device__ __forceinline__ Lane() {
+      const int l = lane_id(), g = l >> 4, i = l & 15, x = C == 64 ? i >> 1 : 0;
+      w = i * RB + (((g >> 1) ^ x) << 4) + 8 * (g & 1);
+      r = i * RB + ((g ^ x) << 4);
+    }
+    __device__ __forceinline__ void fresh() { __asm__ volatile("" : "+v"(w), "+v"(r)); }
+  };
+  // four s from 16 st + 4 g of row r = 16 rt + lane
+  template <int K>
+  __device__ static __forceinline__ void store(const Lane& l, unsigned at, int rt, int st,
+                                               const bf16x4 (&h)[K]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[0][j] = (bf16)x[j];
-}
-__device__ __forceinline__ void to_planes(const float (&x)[8], bf16x8 (&f)[2]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    f[0][j] = (bf16)x[j];
-    f[1][j] = (bf16)(x[j] - (float)f[0][j]);
+    for (int p = 0; p < K; ++p)
+      *lds_at<bf16x4>((l.w ^ st << 5) + (at + p * BYTES + 16 * rt * RB)) = h[p];
   }
+  template <int K>
+  __device__ static __forceinline__ void rows(const Lane& l, unsigned at, int rt, int step,
+                                              bf16x8 (&f)[K]) {
+#pragma unroll
+    for (int p = 0; p < K; ++p)
+      f[p] = *lds_at<bf16x8>((l.r ^ step << 6) + (at + p * BYTES + 16 * rt * RB));
+  }
+};
+
+// Workgroups go to the 8 XCDs in turn, each with an L2 of its own: the roles
+// and the heads of a group, which read the same rows, are a key head's
+// consecutive workgroups on one XCD.
+__device__ __forceinline__ void decay_unit(const DecayScanArgs& a, int& role, int& hk, int& hv,
+                                           int& item) {
+  int y = blockIdx.x / kXcds;
+  role = y % a.roles;
+  y /= a.roles;
+  const int i = y % a.group, Hk = a.Hv / a.group;
+  y = y / a.group * kXcds + blockIdx.x % kXcds;
+  hk = y % Hk;
+  hv = hk * a.group + i;
+  item = y / Hk;
 }
 
 // ------------------------------------------------------------------ the scan
-// Workgroup: one item of one value head.  Wave w owns the state's columns
-// (w_s' index) 16 NDV w .., held transposed in accumulators: tile [b][a] has
-// m = the u index (16 a ..), n = the w index (16 (NDV w + b) ..).
+// Workgroup: one item of one value head, four waves.  Wave w owns NB tiles of
+// 16 columns of the state (its w index), held transposed in accumulators: tile
+// [b][c] has m = the u index (16 c ..), n = the w index (16 (NB w + b) ..).
 //
 // Roundings to fewer bits, for bf16 tensors: P and the state's copy that meets
-// x, whose results are rounded to bf16 themselves; the state itself is summed
-// from w scaled by its decay in two planes (2^-17), since it is an fp32 output
-// and goes on from block to block.
+// x go in two planes (2^-16), whose results are rounded to bf16 themselves;
+// the state, an fp32 output that goes on from block to block, sums w times its
+// decay in three.
+//
+// OUT: a scan; otherwise the sum for a boundary, which is the same whatever
+// order its blocks come in.  They come in the opposite order of the scan's, so
+// that what it reads first is what was read last and (256 MB of it) is still
+// in the last-level cache.
 template <typename T, int D, bool REV, bool OUT>
-__global__ __launch_bounds__(DECAY_NT, 2) void decay_scan_kernel(DecayScanArgs a) {
+__global__ __launch_bounds__(64 * decay_waves<D>(), decay_waves<D>() / 2) void decay_scan_kernel(DecayScanArgs a) {
   typedef DecayTile<T, D> Tl;
-  constexpr int NP = planes<T>(), NDV = D / 16 / DECAY_NW, NDU = D / 16;
-  constexpr int KD = D / 32, KT = BLK / 32;
+  constexpr int C = Tl::C, NP = Tl::NP, NY = DecayKind<T>::NY, NT = Tl::NT;
+  constexpr int NW = NT / 64, NB = D / 16 / NW, NU = D / 16, KD = D / 32, KT = C / 32, NR = C / 16;
+  constexpr int TILES = NR * (NR + 1) / 2, TPW = (TILES + NW - 1) / NW;  // P tiles, of a wave
+  typedef DecayP<C> Pl;
+  // LDS (it starts at 0: there is no other): u, w, x, P, then the powers
+  constexpr unsigned aU = 0, aW = NP * Tl::BYTES, aX = 2 * aW, aP = 3 * aW;
+  constexpr unsigned aF = OUT ? aP + NY * Pl::BYTES : aX;
   extern __shared__ __align__(16) unsigned char smem[];
-  bf16* Us = reinterpret_cast<bf16*>(smem);
-  bf16* Ws = Us + NP * Tl::ELEMS;
-  bf16* Xs = Ws + NP * Tl::ELEMS;
-  bf16* Ps = Xs + NP * Tl::ELEMS;
-  float* pw = reinterpret_cast<float*>(OUT ? Ps + NP * BLK * BLK : Xs);  // a^0 .. a^64, [65] used
-  float* dec = pw + 68;                                                // [64]
+  float* pw = reinterpret_cast<float*>(smem + aF);  // a^0 .. a^C
+  float* dec = pw + C + 4;                          // [C]
 
-  const DecayRole& R = a.role[blockIdx.y];
-  const int hv = blockIdx.x % a.Hv;
+  int role, hk, hv, unit;
+  decay_unit(a, role, hk, hv, unit);
+  const DecayRole& R = a.role[role];
   DecayItem it;
-  if (!decay_item(a.plan, blockIdx.x / a.Hv, it)) return;
+  if (unit >= a.plan.max_items || !decay_item(a.plan, unit, it)) return;
   if (!OUT && (REV ? it.prev : it.next) < 0) return;  // no boundary behind this item
-  const int hk = hv / a.group;
   const int w = wave_id(), lane = lane_id(), g = lane >> 4, li = lane & 15;
-  const int w0 = 16 * NDV * w;  // this wave's first state column
+  const int w0 = 16 * NB * w;  // this wave's first state column
   const float alpha = a.decay[hv];
 
-  f32x4 St[NDV][NDU];
+  const long long xst = R.x.stride, ust = R.u.stride, wst = R.w.stride;
+  const T* xg = nullptr;
+  if constexpr (OUT) xg = reinterpret_cast<const T*>(R.x.p) + it.t0 * xst + (R.x.shared ? hk : hv) * D;
+  const T* ug = reinterpret_cast<const T*>(R.u.p) + it.t0 * ust + (R.u.shared ? hk : hv) * D;
+  const T* wg = reinterpret_cast<const T*>(R.w.p) + it.t0 * wst + (R.w.shared ? hk : hv) * D;
+
+  const int nblk = (it.n + C - 1) / C;
+  const typename Tl::Rows ox(xst), ou(ust), ow(wst);
+  u32x4 rx[OUT ? Tl::NCH : 1], ru[Tl::NCH], rw[Tl::NCH];
+  auto fetch = [&](int b) {
+    const int nv = min(C, it.n - b * C);
+    const long long t = (long long)b * C;
+    Tl::load(ru, ou, Tl::block(ug + t * ust, ust, nv));
+    if constexpr (OUT) Tl::load(rx, ox, Tl::block(xg + t * xst, xst, nv));
+    Tl::load(rw, ow, Tl::block(wg + t * wst, wst, nv));
+  };
+  constexpr bool DOWN = REV == OUT;  // from the last block to the first
+  if (nblk > 0) fetch(DOWN ? nblk - 1 : 0);
+
+  f32x4 St[NB][NU];
   {
     const int slot = REV ? it.next : it.prev;
     const float* E = nullptr;
@@ -266,9 +448,9 @@ __global__ __launch_bounds__(DECAY_NT, 2) void decay_scan_kernel(DecayScanArgs a
       }
     }
 #pragma unroll
-    for (int b = 0; b < NDV; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int c = 0; c < NDU; ++c) {
+      for (int c = 0; c < NU; ++c) {
         const int m = 16 * c + 4 * g, n = w0 + 16 * b + li;
         f32x4 x = {0.f, 0.f, 0.f, 0.f};
         if (E && tr) {
@@ -281,183 +463,185 @@ __global__ __launch_bounds__(DECAY_NT, 2) void decay_scan_kernel(DecayScanArgs a
       }
   }
 
-  const T* xg = nullptr;
-  if constexpr (OUT)
-    xg = reinterpret_cast<const T*>(R.x.p) + (size_t)it.t0 * R.x.stride + (R.x.shared ? hk : hv) * D;
-  const T* ug = reinterpret_cast<const T*>(R.u.p) + (size_t)it.t0 * R.u.stride + (R.u.shared ? hk : hv) * D;
-  const T* wg = reinterpret_cast<const T*>(R.w.p) + (size_t)it.t0 * R.w.stride + (R.w.shared ? hk : hv) * D;
-
-  const int nblk = (it.n + BLK - 1) / BLK;
-  uint4 rx[OUT ? Tl::NCH : 1], ru[Tl::NCH], rw[Tl::NCH];
-  auto fetch = [&](int b) {
-    const int nv = min(BLK, it.n - b * BLK);
-    const size_t t = (size_t)b * BLK;
-    Tl::load(ru, ug + t * R.u.stride, R.u.stride, nv);
-    if constexpr (OUT) Tl::load(rx, xg + t * R.x.stride, R.x.stride, nv);
-    Tl::load(rw, wg + t * R.w.stride, R.w.stride, nv);
-  };
-  if (nblk > 0) fetch(REV ? nblk - 1 : 0);
-
   // powers; P tiles that the mask empties but a product of 32 tokens reads
-  if (threadIdx.x <= BLK) pw[threadIdx.x] = decay_pow(alpha, threadIdx.x);
+  const float s_pair = R.s_pair, s_out = R.s_out;
+  if (threadIdx.x <= C) pw[threadIdx.x] = decay_pow(alpha, threadIdx.x);
   if constexpr (OUT) {
-    for (int i = threadIdx.x; i < NP * BLK * BLK / 8; i += DECAY_NT)
-      reinterpret_cast<uint4*>(Ps)[i] = uint4{0, 0, 0, 0};
+    for (int i = threadIdx.x; i < NY * Pl::BYTES / 16; i += NT)
+      *lds_at<u32x4>(aP + 16 * i) = u32x4{0, 0, 0, 0};
   }
   lds_barrier();
-  float fd[4], fo[4], ft[3];  // a^|r-s| of a diagonal tile (masked), of the next one off, of 16 more
+  // a^(n-1-s) (reversed: a^(s+1)), of whole blocks
+  if (threadIdx.x < C) dec[threadIdx.x] = s_pair * pw[REV ? threadIdx.x + 1 : C - 1 - threadIdx.x];
+  // This wave's tiles of P that the mask leaves (m = s, n = r), in turn; a wave
+  // with one fewer does one twice.  pf: the factors, 0 where a diagonal tile is
+  // masked.
+  int pr[TPW], ps[TPW];
+  float pf[TPW][4];
   if constexpr (OUT) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int d = REV ? 4 * g + e - li : li - 4 * g - e;
-      fd[e] = d >= 0 ? R.s_pair * pw[d] : 0.f;
-      fo[e] = R.s_pair * pw[16 + d];
-    }
+    for (int i = 0; i < TPW; ++i) {
+      int t = w + NW * i;
+      if (t >= TILES) t = max(t - NW, 0) % TILES;
+      const int hi = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, lo = t - hi * (hi + 1) / 2;
+      pr[i] = REV ? lo : hi;
+      ps[i] = REV ? hi : lo;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) ft[i] = pw[16 * i];
+      for (int e = 0; e < 4; ++e) {
+        const int d = 16 * (hi - lo) + (REV ? 4 * g + e - li : li - 4 * g - e);
+        pf[i][e] = d >= 0 ? s_pair * s_out * pw[d] : 0.f;
+      }
+    }
   }
 
+  typename Tl::Lane ln;
+  typename Pl::Lane lp;
+  const double aC = OUT ? 0.0 : decay_pow64(alpha, C);
+  double far = 1.0;  // a sum's block: the decay between it and the boundary
   for (int i = 0; i < nblk; ++i) {
-    const int blk = REV ? nblk - 1 - i : i;
-    const int nv = min(BLK, it.n - blk * BLK);
-    Tl::to_lds(ru, Us, nv);
-    if constexpr (OUT) Tl::to_lds(rx, Xs, nv);
-    Tl::to_lds(rw, Ws, nv);
-    if (threadIdx.x < BLK)
-      dec[threadIdx.x] = R.s_pair * pw[REV ? threadIdx.x + 1 : max(0, nv - 1 - (int)threadIdx.x)];
+    const int blk = DOWN ? nblk - 1 - i : i;
+    const int nv = min(C, it.n - blk * C);
+    Tl::to_lds(ru, aU);
+    if constexpr (OUT) Tl::to_lds(rx, aX);
+    Tl::to_lds(rw, aW);
+    ln.fresh();
+    lp.fresh();
+    if (!REV && nv < C && threadIdx.x < C)  // (w is zero past the end)
+      dec[threadIdx.x] = s_pair * pw[max(0, nv - 1 - (int)threadIdx.x)];
     lds_barrier();
-    if (i + 1 < nblk) fetch(REV ? blk - 1 : blk + 1);
+    if (i + 1 < nblk) fetch(DOWN ? blk - 1 : blk + 1);
 
-    f32x4 O[NDV][4];
+    f32x4 O[NB][NR];
     if constexpr (OUT) {
-      // P: wave w has the pairs of s in its 16 tokens (m = s, n = r)
-      const int r_lo = REV ? 0 : w, r_hi = REV ? w : 3;
-      f32x4 p[4];
+      f32x4 p[TPW];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) p[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < TPW; ++i) p[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < KD; ++s) {
-        bf16x8 fu[NP];
-        Tl::template rows<STD>(Us, 16 * w, s, fu);
+      for (int s = 0; s < KD; ++s)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (j >= r_lo && j <= r_hi) {
-            bf16x8 fx[NP];
-            Tl::template rows<STD>(Xs, 16 * j, s, fx);
-            p[j] = mma_planes(fu, fx, p[j]);
-          }
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j >= r_lo && j <= r_hi) {
-          const int off = REV ? w - j : j - w;
-          float q[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            q[e] = p[j][e] * (off == 0 ? fd[e] : fo[e] * (off == 1 ? ft[0] : off == 2 ? ft[1] : ft[2]));
-          bf16* d = lds_sw(Ps + (16 * j + li) * BLK + 16 * w + 4 * g, BLK);
-          bf16x4 hi;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) hi[e] = (bf16)q[e];
-          *reinterpret_cast<bf16x4*>(d) = hi;
-          if constexpr (NP == 2) {
-            bf16x4 lo;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) lo[e] = (bf16)(q[e] - (float)hi[e]);
-            *reinterpret_cast<bf16x4*>(d + BLK * BLK) = lo;
-          }
+        for (int i = 0; i < TPW; ++i) {
+          bf16x8 fu[NP], fx[NP];
+          Tl::rows_std(ln, aU, 16 * ps[i], s, fu);
+          Tl::rows_std(ln, aX, 16 * pr[i], s, fx);
+          p[i] = mma_planes(fu, fx, p[i]);
         }
+#pragma unroll
+      for (int i = 0; i < TPW; ++i) {
+        const float q[4] = {p[i][0] * pf[i][0], p[i][1] * pf[i][1], p[i][2] * pf[i][2],
+                            p[i][3] * pf[i][3]};
+        bf16x4 h[NY];
+        to_planes(q, h);
+        Pl::store(lp, aP, pr[i], ps[i], h);
+      }
       // E x
       zero_acc(O);
 #pragma unroll
       for (int s = 0; s < KD; ++s) {
-        bf16x8 fs[NDV][NP];
+        bf16x8 fs[NB][NY];
 #pragma unroll
-        for (int b = 0; b < NDV; ++b) {
+        for (int b = 0; b < NB; ++b) {
           const f32x4 lo = St[b][2 * s], hi = St[b][2 * s + 1];
           const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
           to_planes(x, fs[b]);
         }
+        bf16x8 fx[NR][NP];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          bf16x8 fx[NP];
-          Tl::template rows<PERM>(Xs, 16 * j, s, fx);
-#pragma unroll
-          for (int b = 0; b < NDV; ++b) O[b][j] = mma_planes(fs[b], fx, O[b][j]);
-        }
+        for (int j = 0; j < NR; ++j) Tl::rows_perm(ln, aX, 16 * j, s, fx[j]);
+        mma_grid(fs, fx, [&](int b, int j) -> f32x4& { return O[b][j]; });
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < NR; ++j) {
         const int r = 16 * j + li;
-        const float f = pw[REV ? max(0, nv - 1 - r) : r + 1];
+        const float f = s_out * pw[REV ? max(0, nv - 1 - r) : r + 1];
 #pragma unroll
-        for (int b = 0; b < NDV; ++b) O[b][j] *= f;
+        for (int b = 0; b < NB; ++b) O[b][j] *= f;
       }
       lds_barrier();
     }
     // w of this wave's columns: for P w, and scaled for the state
-    const float an = pw[nv];
+    float fd = 1.f;
+    if constexpr (OUT) {
+      const float an = pw[nv];
 #pragma unroll
-    for (int b = 0; b < NDV; ++b)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int c = 0; c < NDU; ++c) St[b][c] *= an;
+        for (int c = 0; c < NU; ++c) St[b][c] *= an;
+    } else {
+      fd = (float)far;
+      far *= aC;
+    }
 #pragma unroll
     for (int s = 0; s < KT; ++s) {
-      bf16x8 fw[NDV][NP], fd2[NDV][2];
-      float dc[8];
+      bf16x8 fw[NB][NP], fs[NB][DECAY_NS];
+      f32x4 d0 = *reinterpret_cast<const f32x4*>(dec + 32 * s + 8 * g);
+      f32x4 d1 = *reinterpret_cast<const f32x4*>(dec + 32 * s + 8 * g + 4);
+      if constexpr (!OUT) {
+        d0 *= fd;
+        d1 *= fd;
+      }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dc[j] = dec[32 * s + 8 * g + j];
-#pragma unroll
-      for (int b = 0; b < NDV; ++b) {
-        Tl::cols(Ws, w0 + 16 * b, s, fw[b]);
+      for (int b = 0; b < NB; ++b) {
+        Tl::cols(ln, aW, NB * w + b, s, fw[b]);
         float x[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          x[j] = (float)fw[b][0][j];
-          if constexpr (NP == 2) x[j] += (float)fw[b][1][j];
-          x[j] *= dc[j];
+          x[j] = (float)fw[b][NP - 1][j];
+#pragma unroll
+          for (int n = NP - 2; n >= 0; --n) x[j] += (float)fw[b][n][j];
+          x[j] *= j < 4 ? d0[j & 3] : d1[j & 3];
         }
-        to_planes(x, fd2[b]);
+        to_planes(x, fs[b]);
       }
       if constexpr (OUT) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < NR; ++j)
           if (REV ? j < 2 * (s + 1) : j >= 2 * s) {
-            bf16x8 fp[NP];
+            bf16x8 fp[NY];
+            Pl::rows(lp, aP, j, s, fp);
 #pragma unroll
-            for (int p = 0; p < NP; ++p)
-              fp[p] = frag_row<bf16, STD>(Ps + p * BLK * BLK + 16 * j * BLK, BLK, s);
-#pragma unroll
-            for (int b = 0; b < NDV; ++b) O[b][j] = mma_planes(fw[b], fp, O[b][j]);
+            for (int b = 0; b < NB; ++b) O[b][j] = mma_planes(fw[b], fp, O[b][j]);
           }
       }
+      constexpr int CG = 4;  // column tiles at a time
 #pragma unroll
-      for (int c = 0; c < NDU; ++c) {
-        bf16x8 fu[NP];
-        Tl::cols(Us, 16 * c, s, fu);
+      for (int c0 = 0; c0 < NU; c0 += CG) {
+        bf16x8 fu[CG][NP];
 #pragma unroll
-        for (int b = 0; b < NDV; ++b) St[b][c] = mma_planes(fu, fd2[b], St[b][c]);
+        for (int c = 0; c < CG; ++c) Tl::cols(ln, aU, c0 + c, s, fu[c]);
+        mma_grid(fu, fs, [&](int c, int b) -> f32x4& { return St[b][c0 + c]; });
       }
     }
+    // y through the x tile to whole rows, or (fp32) straight from the lanes
+    const long long yst = (long long)a.Hv * D;
+    const size_t y0 = (((size_t)it.t0 + blk * C) * a.Hv + hv) * D;
+    const bool rows = OUT && sizeof(T) == 2 && !R.y_f32;
     if constexpr (OUT) {
-      const size_t t = (size_t)it.t0 + blk * BLK;
+      if (rows) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = 16 * j + li;
-        if (r < nv) {
+        for (int j = 0; j < NR; ++j)
 #pragma unroll
-          for (int b = 0; b < NDV; ++b) {
-            const f32x4 y = O[b][j] * R.s_out;
-            const size_t at = ((t + r) * a.Hv + hv) * D + w0 + 16 * b + 4 * g;
-            if (R.y_f32)
-              *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(R.y) + at) = y;
-            else
-              st4(reinterpret_cast<T*>(R.y) + at, y[0], y[1], y[2], y[3]);
+          for (int b = 0; b < NB; ++b) {
+            const f32x4 y = O[b][j];
+            const float q[4] = {y[0], y[1], y[2], y[3]};
+            bf16x4 h[1];
+            to_planes(q, h);
+            *lds_at<bf16x4>((ln.perm ^ (NB * w + b) << 5) + (aX + 16 * j * Tl::RB)) = h[0];
           }
-        }
+      } else {
+        const __amdgpu_buffer_rsrc_t yg = __builtin_amdgcn_make_buffer_rsrc(
+            reinterpret_cast<float*>(R.y) + y0, 0, (int)(((nv - 1) * yst + D) * 4), 0x00020000);
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            __builtin_amdgcn_raw_buffer_store_b128(
+                __builtin_bit_cast(u32x4, O[b][j]), yg,
+                (int)(4 * ((16 * j + li) * (unsigned)yst + w0 + 16 * b + 4 * g)), 0, 0);
       }
     }
     lds_barrier();
+    if (rows)
+      Tl::rows_out(typename Tl::Rows(yst), Tl::block(reinterpret_cast<const T*>(R.y) + y0, yst, nv), aX);
   }
 
   // the exit state: of a sequence's end, or the sum at a boundary
@@ -468,16 +652,17 @@ __global__ __launch_bounds__(DECAY_NT, 2) void decay_scan_kernel(DecayScanArgs a
     out = R.exit + ((size_t)it.seq * a.Hv + hv) * D * D;
   if (out) {
 #pragma unroll
-    for (int b = 0; b < NDV; ++b)
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int c = 0; c < NDU; ++c)
+      for (int c = 0; c < NU; ++c)
         *reinterpret_cast<f32x4*>(out + (size_t)(w0 + 16 * b + li) * D + 16 * c + 4 * g) = St[b][c];
   }
 }
 
 template <typename T, int D, bool OUT> constexpr size_t decay_lds() {
-  return (size_t)planes<T>() * 2 * ((OUT ? 3 : 2) * BLK * D + (OUT ? BLK * BLK : 0)) +
-         (68 + BLK) * sizeof(float);
+  typedef DecayKind<T> K;
+  return (size_t)2 * (K::NP * (OUT ? 3 : 2) * K::C * D + (OUT ? K::NY * K::C * K::C : 0)) +
+         (2 * K::C + 4) * sizeof(float);
 }
 
 // ----------------------------------------------------------------- the chain
@@ -513,7 +698,7 @@ __global__ __launch_bounds__(256) void decay_chain_kernel(DecayChainArgs a) {
   }
   const size_t pitch = (size_t)a.Hv * D * D;
   float* p = R.bound + (size_t)slot0 * pitch + (size_t)hv * D * D + at;
-  constexpr int U = 8;  // boundaries in flight
+  constexpr int U = 16;  // boundaries in flight
   for (int j0 = 0; j0 < cnt; j0 += U) {
     f32x4 n[U];
 #pragma unroll
@@ -524,10 +709,9 @@ __global__ __launch_bounds__(256) void decay_chain_kernel(DecayChainArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u;
-      if (j >= cnt) break;
       X = X * f + n[u];
       f = aL;
-      *reinterpret_cast<f32x4*>(p + (size_t)(R.rev ? cnt - 1 - j : j) * pitch) = X;
+      if (j < cnt) *reinterpret_cast<f32x4*>(p + (size_t)(R.rev ? cnt - 1 - j : j) * pitch) = X;
     }
   }
 }
@@ -565,15 +749,18 @@ static hipError_t decay_plan(const DecayPlan& p, const int* seq_start, int n_seq
 }
 
 template <typename T, int D, bool REV, bool OUT>
-static hipError_t decay_scan(const DecayScanArgs& a, int roles, const char* name, hipStream_t st,
+static hipError_t decay_scan(DecayScanArgs a, int roles, const char* name, hipStream_t st,
                              Profiler* prof) {
   constexpr size_t lds = decay_lds<T, D, OUT>();
   const void* fn = (const void*)decay_scan_kernel<T, D, REV, OUT>;
   hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
+  const long long units = (long long)a.plan.max_items * (a.Hv / a.group);
+  a.roles = roles;
   prof_begin(prof, name, st);
   hipLaunchKernelGGL((decay_scan_kernel<T, D, REV, OUT>),
-                     dim3((unsigned)(a.plan.max_items * a.Hv), roles), dim3(DECAY_NT), lds, st, a);
+                     dim3((unsigned)((units + kXcds - 1) / kXcds * kXcds * a.group * roles)),
+                     dim3(64 * decay_waves<D>()), lds, st, a);
   prof_end(prof, st);
   return hipGetLastError();
 }
@@ -642,8 +829,9 @@ hipError_t launch_decay_bwd(const DecayArgs& d, hipStream_t st, Profiler* prof) 
   b.role[1] = DecayRole{v, dO, q, part ? (void*)d.part[1] : d.dk, f32, d.bound[1], d.dS_out, nullptr,
                         1.f, d.scale, 1, 1};
   if (d.plan.max_multi > 0) {
-    if ((e = decay_scan<T, D, false, false>(f, 1, "decay_sum", st, prof)) != hipSuccess) return e;
+    // (the scan of dq reads v and k next)
     if ((e = decay_scan<T, D, true, false>(b, 1, "decay_sum_rev", st, prof)) != hipSuccess) return e;
+    if ((e = decay_scan<T, D, false, false>(f, 1, "decay_sum", st, prof)) != hipSuccess) return e;
     DecayChainArgs c{};
     c.plan = d.plan;
     c.decay = d.decay;

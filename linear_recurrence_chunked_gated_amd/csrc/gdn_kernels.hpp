@@ -218,7 +218,7 @@ struct DecayRole {
 struct DecayScanArgs {
   DecayPlan plan;
   const float* decay;  // [Hv]
-  int Hv, group;
+  int Hv, group, roles;
   DecayRole role[2];
 };
 struct DecayChainRole {

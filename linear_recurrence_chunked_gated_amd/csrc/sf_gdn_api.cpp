@@ -1211,6 +1211,9 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, DecayCall& c) {
   if ((s = token_stride(p->q_stride, (long long)p->Hk * D, "q", &a.qs)) != SF_OK) return s;
   if ((s = token_stride(p->k_stride, (long long)p->Hk * D, "k", &a.ks)) != SF_OK) return s;
   if ((s = token_stride(p->v_stride, (long long)p->Hv * D, "v", &a.vs)) != SF_OK) return s;
+  // the kernels address a block of 64 rows in 31 bits
+  if (a.qs > (1 << 22) || a.ks > (1 << 22) || a.vs > (1 << 22))
+    return fail(SF_ERR_UNSUPPORTED, "token rows more than 2^22 elements apart");
   a.n_seq = p->n_seq; a.n_tok = p->n_tok; a.Hv = p->Hv; a.group = p->Hv / p->Hk;
   a.scale = p->scale;
   DecayPlan& d = a.plan;
