@@ -35,7 +35,7 @@ struct DecayItem {
 
 __device__ __forceinline__ bool decay_item(const DecayPlan& p, int i, DecayItem& it) {
   if (p.table) {
-    if (i >= p.table[0]) return false;
+    if (i >= p.table[0] && i < p.max_slots) return false;
     const int* e = p.table + kDecayHead + i * kDecayItem;
     it = DecayItem{e[0], e[1], e[2], e[3], e[4]};
     return true;
@@ -85,53 +85,84 @@ __device__ __forceinline__ int scan1024(int x, int* lds, int ident, F join, int&
   return join(before, x);
 }
 
+// Items 0 .. max_slots-1 are the whole segments, by their boundary slot (table[0]
+// of them), then each sequence's last one, those of more blocks first (by the
+// power of two): workgroups start in this order, so that no long item is left
+// for the end.
 __global__ __launch_bounds__(1024) void decay_plan_kernel(const int* seq_start, int n_seq, int n_tok,
-                                                          int L, int max_items, int* table) {
+                                                          DecayPlan p) {
   __shared__ int lds[16];
+  __shared__ int bucket[32];
   auto add = [](int a, int b) { return a + b; };
   auto most = [](int a, int b) { return max(a, b); };
-  int* items = table + kDecayHead;
-  int* multi = items + max_items * kDecayItem;
-  int end = 0, n_items = 0, n_multi = 0;
-  for (int base = 0; base < n_seq; base += 1024) {
-    const int i = base + threadIdx.x;
-    const bool live = i < n_seq;
-    int x = live ? min(max(seq_start[i], 0), n_tok) : 0, top;
-    const int t0 = max(end, scan1024(x, lds, 0, most, top));
-    const int t1 = live ? max(t0, min(max(seq_start[i + 1], 0), n_tok)) : t0;
-    end = max(end, top);
-    const int len = t1 - t0;
-    const int cnt = live ? max(1, (len + L - 1) / L) : 0;
-    int sum, msum;
-    const int at = n_items + scan1024(cnt, lds, 0, add, sum) - cnt;
-    const int many = cnt > 1;
-    const int m = n_multi + scan1024(many, lds, 0, add, msum) - many;
-    // boundary slots before this sequence's: one less than items for each sequence
-    const int slot0 = at - i;
-    if (live)
-      for (int j = 0; j < cnt; ++j) {
-        int* e = items + (at + j) * kDecayItem;
-        e[0] = i;
-        e[1] = t0 + j * L;
-        e[2] = min(L, len - j * L);
-        e[3] = j > 0 ? slot0 + j - 1 : -1;
-        e[4] = j + 1 < cnt ? slot0 + j : -1;
+  int* items = p.table + kDecayHead;
+  int* multi = items + p.max_items * kDecayItem;
+  auto offset = [&](int i) { return min(max(seq_start[i], 0), n_tok); };
+  auto last_of = [&](int len) { return len > 0 ? (len - 1) % p.L + 1 : 0; };  // its tokens
+  auto rank = [&](int tokens) { return __clz((tokens + BLK - 1) / BLK); };    // fewer: later
+  if (threadIdx.x < 32) bucket[threadIdx.x] = 0;
+  // once over the sequences to count the buckets, once to write
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    int end = 0, n_slots = 0, n_multi = 0;
+    __syncthreads();
+    if (pass == 1 && threadIdx.x == 0) {
+      int at = p.max_slots;
+      for (int i = 0; i < 32; ++i) {
+        const int n = bucket[i];
+        bucket[i] = at;
+        at += n;
       }
-    if (many) {
-      int* e = multi + m * kDecayMulti;
-      e[0] = i;
-      e[1] = slot0;
-      e[2] = cnt - 1;
-      e[3] = len - (cnt - 1) * L;
     }
-    n_items += sum;
-    n_multi += msum;
-  }
-  if (threadIdx.x == 0) {
-    table[0] = n_items;
-    table[1] = n_multi;
-    table[2] = n_seq > 0 ? min(max(seq_start[0], 0), n_tok) : 0;  // the rows that sequences have
-    table[3] = max(end, n_seq > 0 ? min(max(seq_start[n_seq], 0), n_tok) : 0);
+    __syncthreads();
+    for (int base = 0; base < n_seq; base += 1024) {
+      const int i = base + threadIdx.x;
+      const bool live = i < n_seq;
+      const int x = live ? offset(i) : 0;
+      int top, slots, multis;
+      const int t0 = max(end, scan1024(x, lds, 0, most, top));
+      const int t1 = live ? max(t0, offset(i + 1)) : t0;
+      end = max(end, top);
+      const int len = t1 - t0, last = last_of(len);
+      if (pass == 0) {
+        if (live) atomicAdd(&bucket[rank(last) & 31], 1);
+        continue;
+      }
+      const int cnt = live && len > 0 ? (len - 1) / p.L : 0;  // whole segments before the last
+      const int slot0 = n_slots + scan1024(cnt, lds, 0, add, slots) - cnt;
+      const int m = n_multi + scan1024(cnt > 0, lds, 0, add, multis) - (cnt > 0);
+      for (int j = 0; j < cnt; ++j) {
+        int* e = items + (slot0 + j) * kDecayItem;
+        e[0] = i;
+        e[1] = t0 + j * p.L;
+        e[2] = p.L;
+        e[3] = j > 0 ? slot0 + j - 1 : -1;
+        e[4] = slot0 + j;
+      }
+      if (live) {
+        int* e = items + atomicAdd(&bucket[rank(last) & 31], 1) * kDecayItem;
+        e[0] = i;
+        e[1] = t0 + cnt * p.L;
+        e[2] = last;
+        e[3] = cnt > 0 ? slot0 + cnt - 1 : -1;
+        e[4] = -1;
+      }
+      if (cnt > 0) {
+        int* e = multi + m * kDecayMulti;
+        e[0] = i;
+        e[1] = slot0;
+        e[2] = cnt;
+        e[3] = last;
+      }
+      n_slots += slots;
+      n_multi += multis;
+    }
+    if (pass == 1 && threadIdx.x == 0) {
+      p.table[0] = n_slots;
+      p.table[1] = n_multi;
+      p.table[2] = n_seq > 0 ? offset(0) : 0;  // the rows that sequences have
+      p.table[3] = max(end, n_seq > 0 ? offset(n_seq) : 0);
+    }
   }
 }
 
@@ -153,7 +184,6 @@ template <> struct DecayKind<float> {
   static constexpr int NP = 3;
   static constexpr int NY = 3;
 };
-constexpr int DECAY_NS = 3;  // planes of w times its decay on the way to the fp32 state
 
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mma_planes(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 c) {
@@ -383,15 +413,16 @@ __device__ __forceinline__ void decay_unit(const DecayScanArgs& a, int& role, in
 // [b][c] has m = the u index (16 c ..), n = the w index (16 (NB w + b) ..).
 //
 // Roundings to fewer bits, for bf16 tensors: P and the state's copy that meets
-// x go in two planes (2^-16), whose results are rounded to bf16 themselves;
-// the state, an fp32 output that goes on from block to block, sums w times its
-// decay in three.
+// x go as bf16 (2^-9), as is usual for operands of outputs that are rounded to
+// bf16 themselves; the state, which goes on from block to block, sums w times
+// its decay in NS = 2 planes (2^-18), and in a third (2^-27) where it ends as an
+// fp32 output, or in a boundary's sum on the way to one.
 //
 // OUT: a scan; otherwise the sum for a boundary, which is the same whatever
 // order its blocks come in.  They come in the opposite order of the scan's, so
 // that what it reads first is what was read last and (256 MB of it) is still
 // in the last-level cache.
-template <typename T, int D, bool REV, bool OUT>
+template <typename T, int D, bool REV, bool OUT, int NS>
 __global__ __launch_bounds__(64 * decay_waves<D>(), decay_waves<D>() / 2) void decay_scan_kernel(DecayScanArgs a) {
   typedef DecayTile<T, D> Tl;
   constexpr int C = Tl::C, NP = Tl::NP, NY = DecayKind<T>::NY, NT = Tl::NT;
@@ -497,7 +528,11 @@ __global__ __launch_bounds__(64 * decay_waves<D>(), decay_waves<D>() / 2) void d
   typename Tl::Lane ln;
   typename Pl::Lane lp;
   const double aC = OUT ? 0.0 : decay_pow64(alpha, C);
-  double far = 1.0;  // a sum's block: the decay between it and the boundary
+  const bool exact = R.exit && (REV ? it.prev : it.next) < 0;  // the state ends as an output
+  // A scan's state is St times `frame`, which takes the blocks' decays until it
+  // leaves 2^-20 .. 2^20 (a sum's block has the decay between it and the
+  // boundary instead).
+  double frame = 1.0, far = 1.0;
   for (int i = 0; i < nblk; ++i) {
     const int blk = DOWN ? nblk - 1 - i : i;
     const int nv = min(C, it.n - blk * C);
@@ -552,33 +587,34 @@ __global__ __launch_bounds__(64 * decay_waves<D>(), decay_waves<D>() / 2) void d
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
         const int r = 16 * j + li;
-        const float f = s_out * pw[REV ? max(0, nv - 1 - r) : r + 1];
+        const float f = s_out * (float)frame * pw[REV ? max(0, nv - 1 - r) : r + 1];
 #pragma unroll
         for (int b = 0; b < NB; ++b) O[b][j] *= f;
       }
       lds_barrier();
     }
     // w of this wave's columns: for P w, and scaled for the state
-    float fd = 1.f;
+    float fd;
     if constexpr (OUT) {
-      const float an = pw[nv];
+      frame *= (double)pw[nv];
+      if (!(frame > 0x1p-20 && frame < 0x1p20)) {
+        const float f = (float)frame;
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int c = 0; c < NU; ++c) St[b][c] *= an;
+          for (int c = 0; c < NU; ++c) St[b][c] *= f;
+        frame = 1.0;
+      }
+      fd = (float)(1.0 / frame);
     } else {
       fd = (float)far;
       far *= aC;
     }
 #pragma unroll
     for (int s = 0; s < KT; ++s) {
-      bf16x8 fw[NB][NP], fs[NB][DECAY_NS];
-      f32x4 d0 = *reinterpret_cast<const f32x4*>(dec + 32 * s + 8 * g);
-      f32x4 d1 = *reinterpret_cast<const f32x4*>(dec + 32 * s + 8 * g + 4);
-      if constexpr (!OUT) {
-        d0 *= fd;
-        d1 *= fd;
-      }
+      bf16x8 fw[NB][NP], fs[NB][NS];
+      const f32x4 d0 = fd * *reinterpret_cast<const f32x4*>(dec + 32 * s + 8 * g);
+      const f32x4 d1 = fd * *reinterpret_cast<const f32x4*>(dec + 32 * s + 8 * g + 4);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         Tl::cols(ln, aW, NB * w + b, s, fw[b]);
@@ -609,6 +645,33 @@ __global__ __launch_bounds__(64 * decay_waves<D>(), decay_waves<D>() / 2) void d
 #pragma unroll
         for (int c = 0; c < CG; ++c) Tl::cols(ln, aU, c0 + c, s, fu[c]);
         mma_grid(fu, fs, [&](int c, int b) -> f32x4& { return St[b][c0 + c]; });
+      }
+    }
+    if constexpr (OUT && NS < 3) {
+      if (exact) {  // what the two planes leave
+#pragma unroll 1
+        for (int s = 0; s < KT; ++s) {
+          bf16x8 f3[NB][1];
+          const float* dp = dec + 32 * s + 8 * g;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            bf16x8 fw[NP];
+            Tl::cols(ln, aW, NB * w + b, s, fw);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float x = (float)fw[0][j] * (fd * dp[j]);
+              x -= (float)(bf16)x;
+              x -= (float)(bf16)x;
+              f3[b][0][j] = (bf16)x;
+            }
+          }
+#pragma unroll
+          for (int c = 0; c < NU; ++c) {
+            bf16x8 fu[1][NP];
+            Tl::cols(ln, aU, c, s, fu[0]);
+            mma_grid(fu, f3, [&](int, int b) -> f32x4& { return St[b][c]; });
+          }
+        }
       }
     }
     // y through the x tile to whole rows, or (fp32) straight from the lanes
@@ -651,11 +714,12 @@ __global__ __launch_bounds__(64 * decay_waves<D>(), decay_waves<D>() / 2) void d
   else if ((REV ? it.prev : it.next) < 0 && R.exit)
     out = R.exit + ((size_t)it.seq * a.Hv + hv) * D * D;
   if (out) {
+    const float f = (float)frame;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int c = 0; c < NU; ++c)
-        *reinterpret_cast<f32x4*>(out + (size_t)(w0 + 16 * b + li) * D + 16 * c + 4 * g) = St[b][c];
+        *reinterpret_cast<f32x4*>(out + (size_t)(w0 + 16 * b + li) * D + 16 * c + 4 * g) = St[b][c] * f;
   }
 }
 
@@ -742,27 +806,39 @@ static hipError_t decay_plan(const DecayPlan& p, const int* seq_start, int n_seq
                              hipStream_t st, Profiler* prof) {
   if (!p.table) return hipSuccess;
   prof_begin(prof, "decay_plan", st);
-  hipLaunchKernelGGL(decay_plan_kernel, dim3(1), dim3(1024), 0, st, seq_start, n_seq, n_tok, p.L,
-                     p.max_items, p.table);
+  hipLaunchKernelGGL(decay_plan_kernel, dim3(1), dim3(1024), 0, st, seq_start, n_seq, n_tok, p);
   prof_end(prof, st);
   return hipGetLastError();
 }
 
-template <typename T, int D, bool REV, bool OUT>
-static hipError_t decay_scan(DecayScanArgs a, int roles, const char* name, hipStream_t st,
-                             Profiler* prof) {
+template <typename T, int D, bool REV, bool OUT, int NS>
+static hipError_t decay_scan_ns(DecayScanArgs a, int roles, const char* name, hipStream_t st,
+                                Profiler* prof) {
   constexpr size_t lds = decay_lds<T, D, OUT>();
-  const void* fn = (const void*)decay_scan_kernel<T, D, REV, OUT>;
+  const void* fn = (const void*)decay_scan_kernel<T, D, REV, OUT, NS>;
   hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
   const long long units = (long long)a.plan.max_items * (a.Hv / a.group);
   a.roles = roles;
   prof_begin(prof, name, st);
-  hipLaunchKernelGGL((decay_scan_kernel<T, D, REV, OUT>),
+  hipLaunchKernelGGL((decay_scan_kernel<T, D, REV, OUT, NS>),
                      dim3((unsigned)((units + kXcds - 1) / kXcds * kXcds * a.group * roles)),
                      dim3(64 * decay_waves<D>()), lds, st, a);
   prof_end(prof, st);
   return hipGetLastError();
+}
+
+// Two planes for the state or three: three in sums for a state that is an
+// output, and in scans where every item ends in one (no sequence is cut);
+// where few do, they take the third by themselves and the others save it
+// (backward of 32,768 tokens, 16 heads, D = 128: 514 us, 534 with three).
+template <typename T, int D, bool REV, bool OUT>
+static hipError_t decay_scan(const DecayScanArgs& a, int roles, const char* name, hipStream_t st,
+                             Profiler* prof) {
+  if constexpr (sizeof(T) == 2)
+    if (OUT ? a.plan.max_multi > 0 : !a.role[0].exit)
+      return decay_scan_ns<T, D, REV, OUT, 2>(a, roles, name, st, prof);
+  return decay_scan_ns<T, D, REV, OUT, 3>(a, roles, name, st, prof);
 }
 
 template <int D>

@@ -188,15 +188,15 @@ int residual_norm_groups(long long N, int C);
 // A call's segments.  Sequences of one length (table null): T tokens in P
 // segments of L.  Packed ones: a table of ints on the device, written by the
 // call's first kernel,
-//   [0] items, [1] sequences of several segments, [2], [3] the rows they have,
-//   max_items items of {sequence, first token, tokens, boundary slots before
-//   and after it (-1: none)}, max_multi of {sequence, first boundary slot,
-//   boundaries, tokens of the last segment}.
+//   [0] boundaries, [1] sequences of several segments, [2], [3] the rows they
+//   have, max_items items of {sequence, first token, tokens, boundary slots
+//   before and after it (-1: none)}, max_multi of {sequence, first boundary
+//   slot, boundaries, tokens of the last segment}.
 constexpr int kDecayHead = 4, kDecayItem = 5, kDecayMulti = 4;
 struct DecayPlan {
   int* table;
   int L, T, P;
-  int max_items, max_multi;
+  int max_items, max_slots, max_multi;
 };
 struct DecayTensor {
   const void* p;

@@ -27,109 +27,116 @@ namespace sfgdn {
 constexpr int ROT_THREADS = 256;
 constexpr int ROT_WAVES = ROT_THREADS / 64;
 
-// Eight cosines and sines of a lane: for columns c .. c+7 of a row.
-// NB (neighbours): columns 2i, 2i+1 share an angle.
-template <bool NB>
-__device__ __forceinline__ void lane_turns(const RotaryArgs& a, int c, long long token,
-                                           float (&co)[NORM_V], float (&si)[NORM_V]) {
+// Cosines and sines of a token's F angles, one or a few per lane, to the
+// wave's part of LDS: cs[0 .. F) and cs[MAX .. MAX + F).  (A lane needs eight,
+// which several lanes share: formed where they are used they would cost eight
+// times as much, half of the forward's arithmetic.)
+constexpr int ROT_MAX = 256;
+__device__ __forceinline__ void token_turns(const RotaryArgs& a, long long token, float* cs) {
   const int pos = a.pos ? a.pos[token] : a.first + (int)(token % a.T);
-#pragma unroll
-  for (int j = 0; j < NORM_V; ++j) {
-    if (NB && j % 2) {
-      co[j] = co[j - 1];
-      si[j] = si[j - 1];
-      continue;
-    }
-    const int i = NB ? (c + j) / 2 : (c < a.F ? c : c - a.F) + j;
+  for (int i = lane_id(); i < a.F; i += 64) {
     const double turns = (double)pos * ((double)a.freq[i] * 0.15915494309189533577);
-    const float f = (float)(turns - rint(turns));
-    sincospif(2.f * f, &si[j], &co[j]);
+    sincospif(2.f * (float)(turns - rint(turns)), &cs[ROT_MAX + i], &cs[i]);
   }
 }
 
-// v turned by the lane's angles (BACK: by the opposite ones).  `other`: the
-// lane with the other halves of its pairs.  Lanes past the rotated columns
-// (!in) keep theirs; every lane of the row calls it.
-template <bool NB, bool BACK>
-__device__ __forceinline__ void turn(float (&v)[NORM_V], const float (&co)[NORM_V],
-                                     const float (&si)[NORM_V], bool in, bool second, int other) {
-  float y[NORM_V];
-#pragma unroll
-  for (int j = 0; j < NORM_V; ++j) {
-    const bool late = NB ? j % 2 : second;  // the second of its pair
-    const float p = NB ? v[j ^ 1] : __shfl(v[j], other);
-    const float s = late != BACK ? si[j] : -si[j];
-    y[j] = v[j] * co[j] + p * s;
+// What a lane is in a row of L lanes.
+template <int L, bool NB> struct RotLane {
+  int c, grp, other;   // first column, row of the wave, byte address of the pairs' other lane
+  bool col, in, late;  // has columns, has rotated ones, the second half of its pairs
+  int first;           // its first angle
+  __device__ __forceinline__ explicit RotLane(const RotaryArgs& a) {
+    const int lane = lane_id();
+    c = lane % L * NORM_V;
+    grp = lane / L;
+    col = c < a.D;
+    in = c < 2 * a.F;
+    late = !NB && in && c >= a.F;
+    other = 4 * (NB || !in ? lane : late ? lane - a.F / NORM_V : lane + a.F / NORM_V);
+    first = !in ? 0 : NB ? c / 2 : late ? c - a.F : c;
   }
+  // its angles' cosines and the sines that its values' partners are taken with
+  __device__ __forceinline__ void angles(const float* cs, float (&co)[NORM_V], float (&si)[NORM_V],
+                                         bool back) const {
 #pragma unroll
-  for (int j = 0; j < NORM_V; ++j) v[j] = in ? y[j] : v[j];
-}
-
-// What a lane is in a row.
-struct RotLane {
-  int c, grp, other;
-  bool col, in, second;
+    for (int j = 0; j < NORM_V; j += 4) {
+      const float* p = cs + first + (NB ? j / 2 : j);
+      float x[4], y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = p[NB ? e / 2 : e];
+        y[e] = p[ROT_MAX + (NB ? e / 2 : e)];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        co[j + e] = in ? x[e] : 1.f;
+        const bool second = NB ? e % 2 : late;
+        si[j + e] = !in ? 0.f : second != back ? y[e] : -y[e];
+      }
+    }
+  }
+  __device__ __forceinline__ void turn(float (&v)[NORM_V], const float (&co)[NORM_V],
+                                       const float (&si)[NORM_V]) const {
+    float p[NORM_V];
+#pragma unroll
+    for (int j = 0; j < NORM_V; ++j)
+      p[j] = NB ? v[j ^ 1]
+                : __int_as_float(__builtin_amdgcn_ds_bpermute(other, __float_as_int(v[j])));
+#pragma unroll
+    for (int j = 0; j < NORM_V; ++j) v[j] = v[j] * co[j] + p[j] * si[j];
+  }
 };
-template <int L>
-__device__ __forceinline__ RotLane rot_lane(const RotaryArgs& a) {
-  RotLane r;
-  const int lane = lane_id();
-  r.c = lane % L * NORM_V;
-  r.grp = lane / L;
-  r.col = r.c < a.D;
-  r.in = r.c < 2 * a.F;
-  r.second = r.c >= a.F;
-  r.other = !r.in ? lane : r.second ? lane - a.F / NORM_V : lane + a.F / NORM_V;
-  return r;
-}
 
-// Head row i of a token: its tensor (0 q, 1 k) and head there.
-__device__ __forceinline__ int rot_side(const RotaryArgs& a, int& h) {
-  if (h < a.H[0]) return 0;
-  h -= a.H[0];
-  return 1;
-}
-
+// A wave takes a token: its query heads, then its key heads, 64 / L at a time,
+// with the next ones' loads ahead.  `split`: heads of a token are spread over
+// so many waves (few tokens).
 template <typename T, int L, bool NB, bool STREAM>
 __global__ __launch_bounds__(ROT_THREADS) void rotary_fwd_kernel(RotaryArgs a, int split) {
   constexpr int G = 64 / L;  // rows of a wave at a time
-  const RotLane r = rot_lane<L>(a);
+  __shared__ float turns[ROT_WAVES][2 * ROT_MAX];
+  float* cs = turns[wave_id()];
+  const RotLane<L, NB> r(a);
   const float inv_d = 1.f / a.D;
-  const int heads = a.H[0] + a.H[1];
-  float w0[NORM_V], w1[NORM_V];
-  fill8(w0, 1.f);
-  fill8(w1, 1.f);
-  if (a.w[0] && r.col) ld8(a.w[0] + r.c, w0);
-  if (a.w[1] && r.col) ld8(a.w[1] + r.c, w1);
+  float w[2][NORM_V];
 #pragma unroll
-  for (int j = 0; j < NORM_V; ++j) {
-    w0[j] *= a.scale[0];
-    w1[j] *= a.scale[1];
+  for (int t = 0; t < 2; ++t) {
+    fill8(w[t], 1.f);
+    if (a.w[t] && r.col) ld8(a.w[t] + r.c, w[t]);
+#pragma unroll
+    for (int j = 0; j < NORM_V; ++j) w[t][j] *= a.scale[t];
   }
-  // work units: a token's heads, or `split` shares of them
   const long long units = a.N * split, step = (long long)gridDim.x * ROT_WAVES;
-  const int share = (heads + G * split - 1) / (G * split) * G;
   for (long long u = (long long)blockIdx.x * ROT_WAVES + wave_id(); u < units; u += step) {
     const long long n = u / split;
-    const int h0 = (int)(u - n * split) * share, h1 = min(heads, h0 + share);
+    const int part = (int)(u - n * split) * G;
     float co[NORM_V], si[NORM_V];
-    if (r.in) lane_turns<NB>(a, r.c, n, co, si);
-    for (int hb = h0; hb < h1; hb += G) {
-      int h = hb + r.grp;
-      const bool live = h < h1 && r.col;
-      const int side = h < h1 ? rot_side(a, h) : 0;
-      Raw8<T> rx;
-      rx.clear();
-      if (live)
-        rx.template load<STREAM>(reinterpret_cast<const T*>(a.x[side]) + n * a.xs[side] + h * a.D + r.c);
-      float x[NORM_V];
-      rx.to(x);
-      const float rstd = rstd_of(sum_lanes<L>(dot8(x, x)), inv_d, a.eps);
+    bool turned = false;
 #pragma unroll
-      for (int j = 0; j < NORM_V; ++j) x[j] *= rstd * (side ? w1[j] : w0[j]);
-      turn<NB, false>(x, co, si, r.in, r.second, r.other);
-      if (live)
-        st8<STREAM>(reinterpret_cast<T*>(a.y[side]) + (n * a.H[side] + h) * a.D + r.c, x);
+    for (int t = 0; t < 2; ++t) {
+      const T* x = reinterpret_cast<const T*>(a.x[t]) + n * a.xs[t] + r.c;
+      T* y = reinterpret_cast<T*>(a.y[t]) + n * a.H[t] * a.D + r.c;
+      Raw8<T> next;
+      auto fetch = [&](int h) {
+        next.clear();
+        if (h < a.H[t] && r.col) next.template load<STREAM>(x + h * a.D);
+      };
+      if (part < a.H[t]) fetch(part + r.grp);
+      if (!turned) {  // behind the first loads
+        token_turns(a, n, cs);
+        r.angles(cs, co, si, false);
+        turned = true;
+      }
+      for (int hb = part; hb < a.H[t]; hb += G * split) {
+        const int h = hb + r.grp;
+        float v[NORM_V];
+        next.to(v);
+        fetch(h + G * split);
+        const float rstd = rstd_of(sum_lanes<L>(dot8(v, v)), inv_d, a.eps);
+#pragma unroll
+        for (int j = 0; j < NORM_V; ++j) v[j] *= rstd * w[t][j];
+        r.turn(v, co, si);
+        if (h < a.H[t] && r.col) st8<STREAM>(y + h * a.D, v);
+      }
     }
   }
 }
@@ -140,66 +147,77 @@ __global__ __launch_bounds__(ROT_THREADS) void rotary_fwd_kernel(RotaryArgs a, i
 template <typename T, int L, bool NB, bool STREAM>
 __global__ __launch_bounds__(ROT_THREADS) void rotary_bwd_kernel(RotaryArgs a) {
   constexpr int G = 64 / L;
-  const RotLane r = rot_lane<L>(a);
+  __shared__ float lds[ROT_THREADS * NORM_V];  // the waves' angles, then the sums
+  static_assert(ROT_WAVES * 2 * ROT_MAX <= ROT_THREADS * NORM_V, "angles fit");
+  float* cs = lds + wave_id() * 2 * ROT_MAX;
+  const RotLane<L, NB> r(a);
   const float inv_d = 1.f / a.D;
-  const int heads = a.H[0] + a.H[1];
-  float w0[NORM_V], w1[NORM_V], dw0[NORM_V], dw1[NORM_V];
-  fill8(w0, 1.f);
-  fill8(w1, 1.f);
-  fill8(dw0, 0.f);
-  fill8(dw1, 0.f);
-  if (a.w[0] && r.col) ld8(a.w[0] + r.c, w0);
-  if (a.w[1] && r.col) ld8(a.w[1] + r.c, w1);
+  float w[2][NORM_V], dw[2][NORM_V];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    fill8(w[t], 1.f);
+    fill8(dw[t], 0.f);
+    if (a.w[t] && r.col) ld8(a.w[t] + r.c, w[t]);
+  }
   for (long long n = (long long)blockIdx.x * ROT_WAVES + wave_id(); n < a.N;
        n += (long long)gridDim.x * ROT_WAVES) {
     float co[NORM_V], si[NORM_V];
-    if (r.in) lane_turns<NB>(a, r.c, n, co, si);
-    for (int hb = 0; hb < heads; hb += G) {
-      int h = hb + r.grp;
-      const bool row = h < heads, live = row && r.col;
-      const int side = row ? rot_side(a, h) : 0;
-      Raw8<T> rx, re;
-      rx.clear();
-      re.clear();
-      if (live) {
-        rx.template load<STREAM>(reinterpret_cast<const T*>(a.x[side]) + n * a.xs[side] + h * a.D + r.c);
-        re.template load<STREAM>(reinterpret_cast<const T*>(a.dy[side]) + (n * a.H[side] + h) * a.D + r.c);
-      }
-      float x[NORM_V], g[NORM_V], t[NORM_V];
-      rx.to(x);
-      re.to(g);
-      turn<NB, true>(g, co, si, r.in, r.second, r.other);
 #pragma unroll
-      for (int j = 0; j < NORM_V; ++j) {
-        g[j] *= side ? a.scale[1] : a.scale[0];
-        t[j] = g[j] * (side ? w1[j] : w0[j]);
+    for (int t = 0; t < 2; ++t) {
+      const T* x = reinterpret_cast<const T*>(a.x[t]) + n * a.xs[t] + r.c;
+      const size_t flat = (size_t)n * a.H[t] * a.D + r.c;
+      const T* dy = reinterpret_cast<const T*>(a.dy[t]) + flat;
+      T* dx = reinterpret_cast<T*>(a.y[t]) + flat;
+      const float scale = a.scale[t];
+      Raw8<T> nx, ne;
+      auto fetch = [&](int h) {
+        nx.clear();
+        ne.clear();
+        if (h < a.H[t] && r.col) {
+          nx.template load<STREAM>(x + h * a.D);
+          ne.template load<STREAM>(dy + h * a.D);
+        }
+      };
+      fetch(r.grp);
+      if (t == 0) {  // behind the first loads
+        token_turns(a, n, cs);
+        r.angles(cs, co, si, true);
       }
-      float rstd = rstd_of(sum_lanes<L>(dot8(x, x)), inv_d, a.eps);
-      if (!row) rstd = 0.f;  // no row: with eps = 0 it would be infinite, and dw NaN
-      const float m = rstd * sum_lanes<L>(dot8(t, x)) * inv_d;
+      for (int hb = 0; hb < a.H[t]; hb += G) {
+        const int h = hb + r.grp;
+        float v[NORM_V], g[NORM_V], e[NORM_V];
+        nx.to(v);
+        ne.to(g);
+        fetch(h + G);
+        r.turn(g, co, si);
 #pragma unroll
-      for (int j = 0; j < NORM_V; ++j) {
-        x[j] *= rstd;
-        const float gn = g[j] * x[j];
-        dw0[j] += side ? 0.f : gn;
-        dw1[j] += side ? gn : 0.f;
-        t[j] = rstd * (t[j] - x[j] * m);
+        for (int j = 0; j < NORM_V; ++j) {
+          g[j] *= scale;
+          e[j] = g[j] * w[t][j];
+        }
+        float rstd = rstd_of(sum_lanes<L>(dot8(v, v)), inv_d, a.eps);
+        if (h >= a.H[t]) rstd = 0.f;  // no row: with eps = 0 it would be infinite, and dw NaN
+        const float m = rstd * sum_lanes<L>(dot8(e, v)) * inv_d;
+#pragma unroll
+        for (int j = 0; j < NORM_V; ++j) {
+          v[j] *= rstd;
+          dw[t][j] += g[j] * v[j];
+          e[j] = rstd * (e[j] - v[j] * m);
+        }
+        if (h < a.H[t] && r.col) st8<STREAM>(dx + h * a.D, e);
       }
-      if (live)
-        st8<STREAM>(reinterpret_cast<T*>(a.y[side]) + (n * a.H[side] + h) * a.D + r.c, t);
     }
   }
   if (!a.dw[0] && !a.dw[1]) return;
-  __shared__ float lds[ROT_THREADS * NORM_V];
   const int two = a.dw[0] && a.dw[1];
   float* out = a.part + (size_t)blockIdx.x * (1 + two) * a.D;
-  if (a.dw[0]) join_groups<L, ROT_THREADS>(dw0, a.D, out, lds);
-  if (a.dw[1]) join_groups<L, ROT_THREADS>(dw1, a.D, out + two * a.D, lds);
+  if (a.dw[0]) join_groups<L, ROT_THREADS>(dw[0], a.D, out, lds);
+  if (a.dw[1]) join_groups<L, ROT_THREADS>(dw[1], a.D, out + two * a.D, lds);
 }
 
 // Workgroups of the backward kernel, each with a row of partial sums: fixed by
 // the shape, so that the sums' order is too.
-constexpr int ROT_GROUPS = 512;
+constexpr int ROT_GROUPS = 768;
 int rotary_groups(long long N) {
   const long long need = (N + ROT_WAVES - 1) / ROT_WAVES;
   return (int)(need < ROT_GROUPS ? need : ROT_GROUPS);
@@ -208,7 +226,7 @@ int rotary_groups(long long N) {
 template <typename T, int L, bool NB, bool STREAM>
 static hipError_t rotary_fwd_l(const RotaryArgs& a, hipStream_t st, Profiler* prof) {
   // few tokens: their heads spread over several waves
-  const int most = (a.H[0] + a.H[1] + 64 / L - 1) / (64 / L);
+  const int most = ((a.H[0] > a.H[1] ? a.H[0] : a.H[1]) + 64 / L - 1) / (64 / L);
   int split = 1;
   while (split < most && a.N * split * 2 <= 2048) split *= 2;
   if (split > most) split = most;

@@ -1222,12 +1222,20 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, DecayCall& c) {
   const long long blocks = ((long long)p->n_tok + BLK - 1) / BLK * p->Hv;
   long long L = (blocks + kDecayGroups - 1) / kDecayGroups;
   if (L < kDecayMinBlocks) L = kDecayMinBlocks;
-  // sequences of one length that fill the GPU by themselves are not cut
-  const long long own = (d.T + BLK - 1) / BLK;
-  if (!packed && ((long long)p->n_seq * p->Hv >= kDecayGroups || L > own)) L = own > 0 ? own : 1;
+  const long long own = (d.T + BLK - 1) / BLK;  // blocks of a sequence
+  if (!packed) {
+    if ((long long)p->n_seq * p->Hv >= kDecayGroups || L >= own) {
+      L = own > 0 ? own : 1;  // sequences that fill the GPU by themselves are not cut
+    } else {
+      // the last segment, which takes longer a block, gets less than the others
+      const long long P = (own + L - 1) / L;
+      L = (2 * own + 2 * P - 2) / (2 * P - 1);
+    }
+  }
   d.L = (int)(L * BLK);
   if (packed) {
     c.slots = p->n_tok > 0 ? (p->n_tok - 1) / d.L : 0;
+    d.max_slots = (int)c.slots;
     d.max_items = p->n_seq + (int)c.slots;
     d.max_multi = (int)(c.slots < p->n_seq ? c.slots : p->n_seq);
     d.P = 0;

@@ -83,22 +83,28 @@ def test_without_entry_state_and_exit_gradient(dtype):
 @pytest.mark.parametrize("B,T,dtype", [(3, 150, "bf16"), (2, 600, "f32"), (1, 64, "bf16"), (2, 0, "f32"),
                                        (0, 7, "f32")])
 def test_one_length(B, T, dtype):
-    """[B, T, H, D] without offsets: the bits of the same sequences packed (at
-    sizes where both are cut alike), and of one sequence without offsets."""
+    """[B, T, H, D] without offsets (cut into other segments than packed rows);
+    [T, H, D] without offsets is one sequence, to the bit."""
     d = chunk_inputs([T] * B, 2, 4, 64, dtype, seed=B + T, grads=True)
     c = _cuda(d)
-    o, S = _fwd(c)
-    grads = _bwd(c)
+    (ro, rS), (ob, Sb) = chunk_ref(d)
+    ref, bnd = chunk_bwd_ref(d)
     e = dict(c, seq_start=None)
     for n in ("q", "k", "v", "dO"):
         e[n] = c[n].reshape(B, T, *c[n].shape[1:])
-    o4, S4 = _fwd(e)
-    assert o4.shape == (B, T, 4, 64) and torch.equal(o4.reshape(o.shape), o) and torch.equal(S4, S)
-    for x, y in zip(_bwd(e), grads):
-        assert torch.equal(x.reshape(y.shape), y)
+    o, S = _fwd(e)
+    assert o.shape == (B, T, 4, 64)
+    check("o", o.reshape(ro.shape), ro, ob, dtype) if o.numel() else None
+    check("S_out", S, rS, Sb, None) if B else None
+    got = _bwd(e)
+    for name, x, r, b in zip(("dq", "dk", "dv", "dS"), got, ref, bnd):
+        assert x.shape == {"dq": e["q"], "dk": e["k"], "dv": e["v"], "dS": S}[name].shape
+        if x.numel():
+            check(name, x.reshape(r.shape), r, b, None if name == "dS" else dtype)
     if B == 1:
-        o3, S3 = _fwd(dict(c, seq_start=None))
-        assert torch.equal(o3, o) and torch.equal(S3, S)
+        flat = dict(c, seq_start=None)
+        for x, y in zip(_fwd(flat) + _bwd(flat), (o, S) + got):
+            assert torch.equal(x, y.reshape(x.shape))
 
 
 def test_many_sequences_of_one_length_are_not_cut():
@@ -204,7 +210,8 @@ def test_more_sequences_than_the_plan_takes_at_once():
     for i in (0, 1, 1022, 1023, 1024, 1025, 2046, 2047, 2048, 2499):
         sl = slice(st[i], st[i + 1])
         one = dict(q=c["q"][sl], k=c["k"][sl], v=c["v"][sl], decay=c["decay"],
-                   S_in=c["S_in"][i:i + 1], seq_start=None)
+                   S_in=c["S_in"][i:i + 1],
+                   seq_start=torch.tensor([0, lens[i]], dtype=torch.int32).cuda())
         o1, S1 = _fwd(one)
         assert torch.equal(o1, o[sl]) and torch.equal(S1[0], S[i]), i
 
