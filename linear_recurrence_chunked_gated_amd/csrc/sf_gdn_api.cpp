@@ -1174,11 +1174,21 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
 // ------------------------------------- linear attention with a decay per head
 namespace {
 
-// Segments of a call.  A scan workgroup takes one item (a segment) of one
-// value head and two share a compute unit, so items of all heads are made
-// about 512, of four blocks at least: shorter ones cost more in boundary
-// states (written, chained and read again) than they give in parallel work.
-constexpr int kDecayGroups = 512, kDecayMinBlocks = 4;
+// Blocks of a segment.  A workgroup takes one segment (an item) of one value
+// head, and two share a compute unit.  Few blocks in all are spread over 256
+// workgroups (1024 tokens of 16 heads at D = 128, forward: 1 block a segment 34
+// us, 4 blocks 44; 4096 tokens: 2 blocks 58 us, 4 blocks 53, 8 blocks 69), more
+// than 8 a segment over 512 (65,536 tokens: 438 us, 523 over 256, 462 over
+// 1024, where boundary states, written, chained and read again, cost more).
+// In bf16 a segment has two blocks at least, and sequences of up to four (fp32:
+// two) are not cut: a block takes less than the two more launches (256 tokens
+// of 2 heads at D = 64: bf16 16 us whole, 20 cut in four; fp32 26 and 21).
+long long decay_blocks(long long blocks, bool f32) {
+  auto over = [&](long long groups) { return (blocks + groups - 1) / groups; };
+  long long L = over(256) < 8 ? over(256) : 8;
+  if (L < over(512)) L = over(512);
+  return L < (f32 ? 1 : 2) ? (f32 ? 1 : 2) : L;
+}
 
 struct DecayCall {
   DecayArgs a;
@@ -1219,15 +1229,16 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, DecayCall& c) {
   DecayPlan& d = a.plan;
   d = DecayPlan{};
   d.T = !packed && p->n_seq > 0 ? p->n_tok / p->n_seq : p->n_tok;
-  const long long blocks = ((long long)p->n_tok + BLK - 1) / BLK * p->Hv;
-  long long L = (blocks + kDecayGroups - 1) / kDecayGroups;
-  if (L < kDecayMinBlocks) L = kDecayMinBlocks;
+  const bool f32 = p->dtype == SF_DTYPE_F32;
+  long long L = decay_blocks(((long long)p->n_tok + BLK - 1) / BLK * p->Hv, f32);
   const long long own = (d.T + BLK - 1) / BLK;  // blocks of a sequence
   if (!packed) {
-    if ((long long)p->n_seq * p->Hv >= kDecayGroups || L >= own) {
-      L = own > 0 ? own : 1;  // sequences that fill the GPU by themselves are not cut
-    } else {
-      // the last segment, which takes longer a block, gets less than the others
+    // sequences that are short, or that fill the GPU by themselves, are not cut
+    if (own <= (f32 ? 2 : 4) || L >= own || (long long)p->n_seq * p->Hv >= 512) {
+      L = own > 0 ? own : 1;
+    } else if (!f32 && L >= 8) {
+      // the last segment, whose state takes a third plane, gets less than the
+      // others (65,536 tokens: the scan 250 us, 287 with segments alike)
       const long long P = (own + L - 1) / L;
       L = (2 * own + 2 * P - 2) / (2 * P - 1);
     }
