@@ -244,13 +244,12 @@ __device__ __forceinline__ bf16x4 lds_tr4(unsigned at) {
   return __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16(lds_at<i16x4>(at)));
 }
 
-// Waves of a workgroup.
-template <int D> constexpr int decay_waves() { return 4; }
+constexpr int DECAY_NW = 4;  // waves of a workgroup
 
 // A block's rows of D values in LDS, in planes of C x D bf16, each row's
 // 16-byte units permuted as by lds_sw.
 template <typename T, int D> struct DecayTile {
-  static constexpr int C = DecayKind<T>::C, NP = DecayKind<T>::NP, NT = 64 * decay_waves<D>();
+  static constexpr int C = DecayKind<T>::C, NP = DecayKind<T>::NP, NT = 64 * DECAY_NW;
   static constexpr int RB = 2 * D, BYTES = C * RB;  // of a plane's row, of a plane
   static constexpr int NW16 = sizeof(T) / 2;        // 16-byte loads for 16 bytes of a plane
   static constexpr int VEC = 16 / (int)sizeof(T), CPR = D / VEC, RPT = NT / CPR, NCH = C / RPT;
@@ -423,7 +422,8 @@ __device__ __forceinline__ void decay_unit(const DecayScanArgs& a, int& role, in
 // that what it reads first is what was read last and (256 MB of it) is still
 // in the last-level cache.
 template <typename T, int D, bool REV, bool OUT, int NS>
-__global__ __launch_bounds__(64 * decay_waves<D>(), decay_waves<D>() / 2) void decay_scan_kernel(DecayScanArgs a) {
+__device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const DecayRole& R, int hk,
+                                                int hv, int unit) {
   typedef DecayTile<T, D> Tl;
   constexpr int C = Tl::C, NP = Tl::NP, NY = DecayKind<T>::NY, NT = Tl::NT;
   constexpr int NW = NT / 64, NB = D / 16 / NW, NU = D / 16, KD = D / 32, KT = C / 32, NR = C / 16;
@@ -436,9 +436,6 @@ __global__ __launch_bounds__(64 * decay_waves<D>(), decay_waves<D>() / 2) void d
   float* pw = reinterpret_cast<float*>(smem + aF);  // a^0 .. a^C
   float* dec = pw + C + 4;                          // [C]
 
-  int role, hk, hv, unit;
-  decay_unit(a, role, hk, hv, unit);
-  const DecayRole& R = a.role[role];
   DecayItem it;
   if (unit >= a.plan.max_items || !decay_item(a.plan, unit, it)) return;
   if (!OUT && (REV ? it.prev : it.next) < 0) return;  // no boundary behind this item
@@ -723,6 +720,25 @@ __global__ __launch_bounds__(64 * decay_waves<D>(), decay_waves<D>() / 2) void d
   }
 }
 
+// Roles that go forward with NSF planes for the state, reversed ones with NSR (0:
+// there are none).
+template <typename T, int D, bool OUT, int NSF, int NSR>
+__global__ __launch_bounds__(64 * DECAY_NW, 2) void decay_scan_kernel(DecayScanArgs a) {
+  int role, hk, hv, unit;
+  decay_unit(a, role, hk, hv, unit);
+  const DecayRole& R = a.role[role];
+  if constexpr (NSF > 0 && NSR > 0) {
+    if (R.rev)
+      decay_scan_item<T, D, true, OUT, NSR>(a, R, hk, hv, unit);
+    else
+      decay_scan_item<T, D, false, OUT, NSF>(a, R, hk, hv, unit);
+  } else if constexpr (NSF > 0) {
+    decay_scan_item<T, D, false, OUT, NSF>(a, R, hk, hv, unit);
+  } else {
+    decay_scan_item<T, D, true, OUT, NSR>(a, R, hk, hv, unit);
+  }
+}
+
 template <typename T, int D, bool OUT> constexpr size_t decay_lds() {
   typedef DecayKind<T> K;
   return (size_t)2 * (K::NP * (OUT ? 3 : 2) * K::C * D + (OUT ? K::NY * K::C * K::C : 0)) +
@@ -811,34 +827,49 @@ static hipError_t decay_plan(const DecayPlan& p, const int* seq_start, int n_seq
   return hipGetLastError();
 }
 
-template <typename T, int D, bool REV, bool OUT, int NS>
-static hipError_t decay_scan_ns(DecayScanArgs a, int roles, const char* name, hipStream_t st,
-                                Profiler* prof) {
+template <typename T, int D, bool OUT, int NSF, int NSR>
+static hipError_t decay_scan(DecayScanArgs a, const char* name, hipStream_t st, Profiler* prof) {
   constexpr size_t lds = decay_lds<T, D, OUT>();
-  const void* fn = (const void*)decay_scan_kernel<T, D, REV, OUT, NS>;
+  const void* fn = (const void*)decay_scan_kernel<T, D, OUT, NSF, NSR>;
   hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
   if (e != hipSuccess) return e;
   const long long units = (long long)a.plan.max_items * (a.Hv / a.group);
-  a.roles = roles;
   prof_begin(prof, name, st);
-  hipLaunchKernelGGL((decay_scan_kernel<T, D, REV, OUT, NS>),
-                     dim3((unsigned)((units + kXcds - 1) / kXcds * kXcds * a.group * roles)),
-                     dim3(64 * decay_waves<D>()), lds, st, a);
+  hipLaunchKernelGGL((decay_scan_kernel<T, D, OUT, NSF, NSR>),
+                     dim3((unsigned)((units + kXcds - 1) / kXcds * kXcds * a.group * a.roles)),
+                     dim3(64 * DECAY_NW), lds, st, a);
   prof_end(prof, st);
   return hipGetLastError();
 }
 
-// Two planes for the state or three: three in sums for a state that is an
-// output, and in scans where every item ends in one (no sequence is cut);
-// where few do, they take the third by themselves and the others save it
-// (backward of 32,768 tokens, 16 heads, D = 128: 514 us, 534 with three).
-template <typename T, int D, bool REV, bool OUT>
-static hipError_t decay_scan(const DecayScanArgs& a, int roles, const char* name, hipStream_t st,
-                             Profiler* prof) {
-  if constexpr (sizeof(T) == 2)
-    if (OUT ? a.plan.max_multi > 0 : !a.role[0].exit)
-      return decay_scan_ns<T, D, REV, OUT, 2>(a, roles, name, st, prof);
-  return decay_scan_ns<T, D, REV, OUT, 3>(a, roles, name, st, prof);
+// Planes of the state (bf16): three in sums for a state that is an output, and
+// in scans where every item ends in one (no sequence is cut); where few do, they
+// take the third by themselves and the others save it (backward of 32,768
+// tokens, 16 heads, D = 128: 503 us, 534 with three).  A scan of dq ends in none.
+template <typename T, int D>
+static hipError_t decay_sums(const DecayScanArgs& a, bool bwd, bool exit, hipStream_t st, Profiler* prof) {
+  if constexpr (sizeof(T) == 4)
+    return bwd ? decay_scan<T, D, false, 3, 3>(a, "decay_sum_bwd", st, prof)
+               : decay_scan<T, D, false, 3, 0>(a, "decay_sum", st, prof);
+  else if (bwd)
+    return exit ? decay_scan<T, D, false, 2, 3>(a, "decay_sum_bwd", st, prof)
+                : decay_scan<T, D, false, 2, 2>(a, "decay_sum_bwd", st, prof);
+  else
+    return exit ? decay_scan<T, D, false, 3, 0>(a, "decay_sum", st, prof)
+                : decay_scan<T, D, false, 2, 0>(a, "decay_sum", st, prof);
+}
+template <typename T, int D>
+static hipError_t decay_scans(const DecayScanArgs& a, bool bwd, bool exit, hipStream_t st, Profiler* prof) {
+  const bool third = exit && a.plan.max_multi == 0;
+  if constexpr (sizeof(T) == 4)
+    return bwd ? decay_scan<T, D, true, 3, 3>(a, "decay_scan_bwd", st, prof)
+               : decay_scan<T, D, true, 3, 0>(a, "decay_scan", st, prof);
+  else if (bwd)
+    return third ? decay_scan<T, D, true, 2, 3>(a, "decay_scan_bwd", st, prof)
+                 : decay_scan<T, D, true, 2, 2>(a, "decay_scan_bwd", st, prof);
+  else
+    return third ? decay_scan<T, D, true, 3, 0>(a, "decay_scan", st, prof)
+                 : decay_scan<T, D, true, 2, 0>(a, "decay_scan", st, prof);
 }
 
 template <int D>
@@ -860,19 +891,11 @@ hipError_t launch_decay_fwd(const DecayArgs& d, hipStream_t st, Profiler* prof) 
   a.decay = d.decay;
   a.Hv = d.Hv;
   a.group = d.group;
-  DecayRole& r = a.role[0];
-  r.x = {d.q, d.qs, 1};
-  r.u = {d.k, d.ks, 1};
-  r.w = {d.v, d.vs, 0};
-  r.y = d.o;
-  r.y_f32 = sizeof(T) == 4;
-  r.bound = d.bound[0];
-  r.state = d.S_in;
-  r.exit = d.S_out;
-  r.s_out = d.scale;
-  r.s_pair = 1.f;
+  a.roles = 1;
+  a.role[0] = DecayRole{{d.q, d.qs, 1}, {d.k, d.ks, 1}, {d.v, d.vs, 0}, d.o, sizeof(T) == 4,
+                        d.bound[0],     d.S_in,         d.S_out,        d.scale, 1.f, 0, 0, 0};
   if (d.plan.max_multi > 0) {
-    if ((e = decay_scan<T, D, false, false>(a, 1, "decay_sum", st, prof)) != hipSuccess) return e;
+    if ((e = decay_sums<T, D>(a, false, d.S_out, st, prof)) != hipSuccess) return e;
     DecayChainArgs c{};
     c.plan = d.plan;
     c.decay = d.decay;
@@ -880,7 +903,7 @@ hipError_t launch_decay_fwd(const DecayArgs& d, hipStream_t st, Profiler* prof) 
     c.role[0] = DecayChainRole{d.bound[0], d.S_in, 0, 0};
     if ((e = decay_chain<D>(c, 1, st, prof)) != hipSuccess) return e;
   }
-  return decay_scan<T, D, false, true>(a, 1, "decay_scan", st, prof);
+  return decay_scans<T, D>(a, false, d.S_out, st, prof);
 }
 
 template <typename T, int D>
@@ -891,23 +914,22 @@ hipError_t launch_decay_bwd(const DecayArgs& d, hipStream_t st, Profiler* prof) 
       dO{d.dO, (long long)d.Hv * D, 0};
   const bool part = d.group > 1;
   const int f32 = part || sizeof(T) == 4;
-  DecayScanArgs f{}, b{};
-  f.plan = b.plan = d.plan;
-  f.decay = b.decay = d.decay;
-  f.Hv = b.Hv = d.Hv;
-  f.group = b.group = d.group;
-  // dq: the forward scan of S^T
-  f.role[0] = DecayRole{dO, v, k, part ? (void*)d.part[0] : d.dq, f32, d.bound[0], d.S_in, nullptr,
-                        d.scale, 1.f, 1, 0};
+  DecayScanArgs a{};
+  a.plan = d.plan;
+  a.decay = d.decay;
+  a.Hv = d.Hv;
+  a.group = d.group;
   // dv and dk: the reversed scan of G and of G^T, from the same boundaries
-  b.role[0] = DecayRole{k, q, dO, d.dv, sizeof(T) == 4, d.bound[1], d.dS_out, d.dS_in, 1.f, d.scale,
-                        0, 0};
-  b.role[1] = DecayRole{v, dO, q, part ? (void*)d.part[1] : d.dk, f32, d.bound[1], d.dS_out, nullptr,
-                        1.f, d.scale, 1, 1};
+  a.role[0] = DecayRole{k, q, dO, d.dv, sizeof(T) == 4, d.bound[1], d.dS_out, d.dS_in, 1.f, d.scale,
+                        0, 0, 1};
+  a.role[2] = DecayRole{v, dO, q, part ? (void*)d.part[1] : d.dk, f32, d.bound[1], d.dS_out, nullptr,
+                        1.f, d.scale, 1, 1, 1};
+  // dq: the forward scan of S^T
+  a.role[1] = DecayRole{dO, v, k, part ? (void*)d.part[0] : d.dq, f32, d.bound[0], d.S_in, nullptr,
+                        d.scale, 1.f, 1, 0, 0};
   if (d.plan.max_multi > 0) {
-    // (the scan of dq reads v and k next)
-    if ((e = decay_scan<T, D, true, false>(b, 1, "decay_sum_rev", st, prof)) != hipSuccess) return e;
-    if ((e = decay_scan<T, D, false, false>(f, 1, "decay_sum", st, prof)) != hipSuccess) return e;
+    a.roles = 2;
+    if ((e = decay_sums<T, D>(a, true, d.dS_in, st, prof)) != hipSuccess) return e;
     DecayChainArgs c{};
     c.plan = d.plan;
     c.decay = d.decay;
@@ -916,8 +938,8 @@ hipError_t launch_decay_bwd(const DecayArgs& d, hipStream_t st, Profiler* prof) 
     c.role[1] = DecayChainRole{d.bound[1], d.dS_out, 0, 1};
     if ((e = decay_chain<D>(c, 2, st, prof)) != hipSuccess) return e;
   }
-  if ((e = decay_scan<T, D, false, true>(f, 1, "decay_scan_dq", st, prof)) != hipSuccess) return e;
-  if ((e = decay_scan<T, D, true, true>(b, 2, "decay_scan_dkv", st, prof)) != hipSuccess) return e;
+  a.roles = 3;
+  if ((e = decay_scans<T, D>(a, true, d.dS_in, st, prof)) != hipSuccess) return e;
   if (!part || d.n_tok == 0) return hipSuccess;
   DecayGroupArgs g{};
   g.plan = d.plan;

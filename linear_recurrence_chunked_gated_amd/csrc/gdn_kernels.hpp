@@ -214,12 +214,13 @@ struct DecayRole {
   float* exit;         // the same after the last one, or null
   float s_out, s_pair;  // factors of y, and of every product w u
   int tr_state, tr_bound;
+  int rev;
 };
 struct DecayScanArgs {
   DecayPlan plan;
   const float* decay;  // [Hv]
   int Hv, group, roles;
-  DecayRole role[2];
+  DecayRole role[3];
 };
 struct DecayChainRole {
   float* bound;

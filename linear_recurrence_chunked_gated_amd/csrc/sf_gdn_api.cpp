@@ -1175,18 +1175,24 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
 namespace {
 
 // Blocks of a segment.  A workgroup takes one segment (an item) of one value
-// head, and two share a compute unit.  Few blocks in all are spread over 256
-// workgroups (1024 tokens of 16 heads at D = 128, forward: 1 block a segment 34
-// us, 4 blocks 44; 4096 tokens: 2 blocks 58 us, 4 blocks 53, 8 blocks 69), more
-// than 8 a segment over 512 (65,536 tokens: 438 us, 523 over 256, 462 over
-// 1024, where boundary states, written, chained and read again, cost more).
+// head and, in a backward, one of the three gradients; two share a compute unit.
+// Few blocks in all are spread over 256 workgroups (forward of 1024 tokens of 16
+// heads at D = 128: 1 block a segment 34 us, 4 blocks 44; 4096 tokens: 2 blocks
+// 58 us, 4 blocks 53, 8 blocks 69), more than 8 a segment over 512 (65,536
+// tokens: 438 us, 523 over 256, 462 over 1024, where boundary states, written,
+// chained and read again, cost more).  A backward in bf16 takes a third of that,
+// one round of its three scans (backward of 16,384 tokens of 16 heads 241 us, 262
+// over 512; 24 packed sequences of 16,411 tokens, 32 heads: 505 and 545; but of
+// 65,536 tokens 890 and 857); in fp32, where the scans are bound by
+// their products, it does not (32,768 tokens 1185 us, 1350 over 170).
 // In bf16 a segment has two blocks at least, and sequences of up to four (fp32:
 // two) are not cut: a block takes less than the two more launches (256 tokens
 // of 2 heads at D = 64: bf16 16 us whole, 20 cut in four; fp32 26 and 21).
-long long decay_blocks(long long blocks, bool f32) {
+long long decay_blocks(long long blocks, bool f32, bool bwd) {
   auto over = [&](long long groups) { return (blocks + groups - 1) / groups; };
-  long long L = over(256) < 8 ? over(256) : 8;
-  if (L < over(512)) L = over(512);
+  const int some = bwd && !f32 ? 170 : 256, all = bwd && !f32 ? 170 : 512;
+  long long L = over(some) < 8 ? over(some) : 8;
+  if (L < over(all)) L = over(all);
   return L < (f32 ? 1 : 2) ? (f32 ? 1 : 2) : L;
 }
 
@@ -1198,7 +1204,7 @@ struct DecayCall {
   size_t part;
 };
 
-sf_status make_decay(const sf_decay_shape* p, bool packed, DecayCall& c) {
+sf_status make_decay(const sf_decay_shape* p, bool packed, bool bwd, DecayCall& c) {
   if (!p) return fail(SF_ERR_INVALID_ARG, "shape is NULL");
   sf_status s;
   if ((s = check_dtype(p->dtype)) != SF_OK) return s;
@@ -1230,11 +1236,16 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, DecayCall& c) {
   d = DecayPlan{};
   d.T = !packed && p->n_seq > 0 ? p->n_tok / p->n_seq : p->n_tok;
   const bool f32 = p->dtype == SF_DTYPE_F32;
-  long long L = decay_blocks(((long long)p->n_tok + BLK - 1) / BLK * p->Hv, f32);
+  long long L = decay_blocks(((long long)p->n_tok + BLK - 1) / BLK * p->Hv, f32, bwd);
   const long long own = (d.T + BLK - 1) / BLK;  // blocks of a sequence
   if (!packed) {
-    // sequences that are short, or that fill the GPU by themselves, are not cut
-    if (own <= (f32 ? 2 : 4) || L >= own || (long long)p->n_seq * p->Hv >= 512) {
+    // Sequences that are short, or that fill three quarters of the GPU by
+    // themselves, are not cut: there is no pass for boundary states then, and a
+    // workgroup alone on its compute unit is faster (forward of 2048 tokens each,
+    // 16 heads: 12 sequences 150 us, 171 cut, 8 sequences 144 and 115; backward,
+    // three workgroups to a head: 8 sequences 202 us, 277 cut, 4 of 4096 tokens
+    // 276 and 262).
+    if (own <= (f32 ? 2 : 4) || L >= own || (long long)p->n_seq * p->Hv >= (bwd ? 96 : 192)) {
       L = own > 0 ? own : 1;
     } else if (!f32 && L >= 8) {
       // the last segment, whose state takes a third plane, gets less than the
@@ -1271,12 +1282,12 @@ size_t decay_ws(const DecayCall& c, bool bwd) {
 // Bytes for either kind of batch: the shape does not say which it is.
 sf_status decay_ws_size(const sf_decay_shape* shape, bool bwd, size_t* bytes) {
   DecayCall c{};
-  sf_status s = make_decay(shape, true, c);
+  sf_status s = make_decay(shape, true, bwd, c);
   if (s != SF_OK) return s;
   if (!bytes) return fail(SF_ERR_INVALID_ARG, "bytes is NULL");
   *bytes = decay_ws(c, bwd);
   if (shape->n_seq > 0 && shape->n_tok % shape->n_seq == 0) {
-    if ((s = make_decay(shape, false, c)) != SF_OK) return s;
+    if ((s = make_decay(shape, false, bwd, c)) != SF_OK) return s;
     if (decay_ws(c, bwd) > *bytes) *bytes = decay_ws(c, bwd);
   }
   return SF_OK;
@@ -1329,7 +1340,7 @@ sf_status sf_gdn_decay_chunk_fwd(const sf_decay_shape* shape, const void* q, con
                                  const float* S_in, void* o, float* S_out, void* workspace,
                                  size_t ws_bytes, void* stream) try {
   DecayCall c{};
-  sf_status s = make_decay(shape, seq_start != nullptr, c);
+  sf_status s = make_decay(shape, seq_start != nullptr, false, c);
   if (s != SF_OK) return s;
   const sf_decay_shape& p = *shape;
   DecayArgs& a = c.a;
@@ -1374,7 +1385,7 @@ sf_status sf_gdn_decay_chunk_bwd(const sf_decay_shape* shape, const void* q, con
                                  void* dk, void* dv, float* dS_in, void* workspace,
                                  size_t ws_bytes, void* stream) try {
   DecayCall c{};
-  sf_status s = make_decay(shape, seq_start != nullptr, c);
+  sf_status s = make_decay(shape, seq_start != nullptr, true, c);
   if (s != SF_OK) return s;
   const sf_decay_shape& p = *shape;
   DecayArgs& a = c.a;
