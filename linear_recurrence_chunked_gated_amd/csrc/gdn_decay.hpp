@@ -33,20 +33,81 @@ struct DecayItem {
   int seq, t0, n, prev, next;
 };
 
-__device__ __forceinline__ bool decay_item(const DecayPlan& p, int i, DecayItem& it) {
-  if (p.table) {
-    if (i >= p.table[0] && i < p.max_slots) return false;
-    const int* e = p.table + kDecayHead + i * kDecayItem;
-    it = DecayItem{e[0], e[1], e[2], e[3], e[4]};
-    return true;
+// Packed sequences: offsets are taken as their running maximum, clamped to the
+// token rows, so that items never overlap or reach outside them, whatever
+// seq_start holds.
+__device__ __forceinline__ int decay_offset(const DecayPlan& p, int i) {
+  return min(max(p.seq_start[i], 0), p.n_tok);
+}
+// The last segments' rank falls with their blocks (by the power of two): the
+// longer ones come first, so that no long item is left for the end.
+__device__ __forceinline__ int decay_rank(int tokens) { return __clz((tokens + BLK - 1) / BLK); }
+
+// x joined with the lanes before: rows of 16, then their ends to the next ones.
+template <typename F> __device__ __forceinline__ int wave_scan(int x, int ident, F join) {
+  x = join(x, __builtin_amdgcn_update_dpp(ident, x, 0x111, 0xF, 0xF, false));
+  x = join(x, __builtin_amdgcn_update_dpp(ident, x, 0x112, 0xF, 0xF, false));
+  x = join(x, __builtin_amdgcn_update_dpp(ident, x, 0x114, 0xF, 0xF, false));
+  x = join(x, __builtin_amdgcn_update_dpp(ident, x, 0x118, 0xF, 0xF, false));
+  x = join(x, __builtin_amdgcn_update_dpp(ident, x, 0x142, 0xA, 0xF, false));
+  return join(x, __builtin_amdgcn_update_dpp(ident, x, 0x143, 0xC, 0xF, false));
+}
+
+// Up to 64 sequences, one a lane: every wave plans for itself, which takes less
+// than a kernel before the others would (9 sequences, 4099 tokens in all, 6 heads
+// at D = 64 in fp32: 37 us with one, 33 so; backward 57 and 53).
+struct DecaySeqs {
+  int t0, t1, cnt, slot0;  // its rows, its whole segments before the last, their first slot
+  __device__ __forceinline__ DecaySeqs(const DecayPlan& p) {
+    const int i = lane_id();
+    const bool live = i < p.n_seq;
+    const int x = live ? decay_offset(p, i) : 0, y = live ? decay_offset(p, i + 1) : 0;
+    t0 = wave_scan(x, 0, [](int a, int b) { return max(a, b); });
+    t1 = max(t0, y);
+    cnt = live && t1 > t0 ? (t1 - t0 - 1) / p.L : 0;
+    slot0 = wave_scan(cnt, 0, [](int a, int b) { return a + b; }) - cnt;
   }
-  const int seq = i / p.P, j = i - seq * p.P;
-  it.seq = seq;
-  it.t0 = seq * p.T + j * p.L;
-  it.n = min(p.L, p.T - j * p.L);
-  it.prev = j > 0 ? seq * (p.P - 1) + j - 1 : -1;
-  it.next = j + 1 < p.P ? seq * (p.P - 1) + j : -1;
-  return true;
+};
+
+// Item i (none: a negative sequence).  Packed: 0 .. max_slots-1 are the whole
+// segments, by their boundary slot, then each sequence's last one, by its rank.
+__device__ __forceinline__ DecayItem decay_item(const DecayPlan& p, int i) {
+  if (p.table) {
+    const int* e = p.table + kDecayHead + i * kDecayItem;
+    return DecayItem{i >= p.table[0] && i < p.max_slots ? -1 : e[0], e[1], e[2], e[3], e[4]};
+  }
+  int seq, t0, len, first, cnt, j;
+  if (p.seq_start) {
+    const DecaySeqs s(p);
+    unsigned long long in = __ballot(i >= s.slot0 && i < s.slot0 + s.cnt);
+    if (i >= p.max_slots) {
+      const int rank = lane_id() < p.n_seq ? decay_rank(s.t1 - s.t0 - s.cnt * p.L) : -1;
+      int before = i - p.max_slots;
+      for (int r = decay_rank(p.L); r <= 32; ++r) {
+        in = __ballot(rank == r);
+        const int n = __builtin_popcountll(in);
+        if (before < n) break;
+        before -= n;
+      }
+      for (; before > 0; --before) in &= in - 1;
+    }
+    seq = in ? __builtin_ctzll(in) : 0;
+    t0 = __builtin_amdgcn_readlane(s.t0, seq);
+    len = __builtin_amdgcn_readlane(s.t1, seq) - t0;
+    first = __builtin_amdgcn_readlane(s.slot0, seq);
+    cnt = __builtin_amdgcn_readlane(s.cnt, seq);
+    j = i < p.max_slots ? i - first : cnt;
+    if (!in) seq = -1;
+  } else {
+    seq = i / p.P;
+    j = i - seq * p.P;
+    t0 = seq * p.T;
+    len = p.T;
+    cnt = p.P - 1;
+    first = seq * cnt;
+  }
+  return DecayItem{seq, t0 + j * p.L, j < cnt ? p.L : len - cnt * p.L, j > 0 ? first + j - 1 : -1,
+                   j < cnt ? first + j : -1};
 }
 
 // a^e for e >= 0, by squaring in 64 bits: exact to a rounding for every a,
@@ -63,9 +124,7 @@ __device__ __forceinline__ double decay_pow64(float a, int e) {
 __device__ __forceinline__ float decay_pow(float a, int e) { return (float)decay_pow64(a, e); }
 
 // ------------------------------------------------------------------ the plan
-// Items and boundary slots of packed sequences, by one workgroup.  Offsets are
-// taken as their running maximum, clamped to the token rows, so that items
-// never overlap or reach outside them, whatever seq_start holds.
+// Items and boundary slots of more packed sequences, by one workgroup.
 template <typename F>
 __device__ __forceinline__ int scan1024(int x, int* lds, int ident, F join, int& total) {
   const int lane = lane_id(), w = wave_id();
@@ -85,21 +144,14 @@ __device__ __forceinline__ int scan1024(int x, int* lds, int ident, F join, int&
   return join(before, x);
 }
 
-// Items 0 .. max_slots-1 are the whole segments, by their boundary slot (table[0]
-// of them), then each sequence's last one, those of more blocks first (by the
-// power of two): workgroups start in this order, so that no long item is left
-// for the end.
-__global__ __launch_bounds__(1024) void decay_plan_kernel(const int* seq_start, int n_seq, int n_tok,
-                                                          DecayPlan p) {
+__global__ __launch_bounds__(1024) void decay_plan_kernel(DecayPlan p) {
   __shared__ int lds[16];
   __shared__ int bucket[32];
   auto add = [](int a, int b) { return a + b; };
   auto most = [](int a, int b) { return max(a, b); };
   int* items = p.table + kDecayHead;
   int* multi = items + p.max_items * kDecayItem;
-  auto offset = [&](int i) { return min(max(seq_start[i], 0), n_tok); };
-  auto last_of = [&](int len) { return len > 0 ? (len - 1) % p.L + 1 : 0; };  // its tokens
-  auto rank = [&](int tokens) { return __clz((tokens + BLK - 1) / BLK); };    // fewer: later
+  const int n_seq = p.n_seq;
   if (threadIdx.x < 32) bucket[threadIdx.x] = 0;
   // once over the sequences to count the buckets, once to write
 #pragma unroll 1
@@ -118,17 +170,17 @@ __global__ __launch_bounds__(1024) void decay_plan_kernel(const int* seq_start, 
     for (int base = 0; base < n_seq; base += 1024) {
       const int i = base + threadIdx.x;
       const bool live = i < n_seq;
-      const int x = live ? offset(i) : 0;
+      const int x = live ? decay_offset(p, i) : 0;
       int top, slots, multis;
       const int t0 = max(end, scan1024(x, lds, 0, most, top));
-      const int t1 = live ? max(t0, offset(i + 1)) : t0;
+      const int t1 = live ? max(t0, decay_offset(p, i + 1)) : t0;
       end = max(end, top);
-      const int len = t1 - t0, last = last_of(len);
+      const int len = t1 - t0, cnt = live && len > 0 ? (len - 1) / p.L : 0;
+      const int last = len - cnt * p.L;
       if (pass == 0) {
-        if (live) atomicAdd(&bucket[rank(last) & 31], 1);
+        if (live) atomicAdd(&bucket[decay_rank(last) & 31], 1);
         continue;
       }
-      const int cnt = live && len > 0 ? (len - 1) / p.L : 0;  // whole segments before the last
       const int slot0 = n_slots + scan1024(cnt, lds, 0, add, slots) - cnt;
       const int m = n_multi + scan1024(cnt > 0, lds, 0, add, multis) - (cnt > 0);
       for (int j = 0; j < cnt; ++j) {
@@ -140,7 +192,7 @@ __global__ __launch_bounds__(1024) void decay_plan_kernel(const int* seq_start, 
         e[4] = slot0 + j;
       }
       if (live) {
-        int* e = items + atomicAdd(&bucket[rank(last) & 31], 1) * kDecayItem;
+        int* e = items + atomicAdd(&bucket[decay_rank(last) & 31], 1) * kDecayItem;
         e[0] = i;
         e[1] = t0 + cnt * p.L;
         e[2] = last;
@@ -160,8 +212,8 @@ __global__ __launch_bounds__(1024) void decay_plan_kernel(const int* seq_start, 
     if (pass == 1 && threadIdx.x == 0) {
       p.table[0] = n_slots;
       p.table[1] = n_multi;
-      p.table[2] = n_seq > 0 ? offset(0) : 0;  // the rows that sequences have
-      p.table[3] = max(end, n_seq > 0 ? offset(n_seq) : 0);
+      p.table[2] = n_seq > 0 ? decay_offset(p, 0) : 0;  // the rows that sequences have
+      p.table[3] = max(end, n_seq > 0 ? decay_offset(p, n_seq) : 0);
     }
   }
 }
@@ -436,8 +488,9 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
   float* pw = reinterpret_cast<float*>(smem + aF);  // a^0 .. a^C
   float* dec = pw + C + 4;                          // [C]
 
-  DecayItem it;
-  if (unit >= a.plan.max_items || !decay_item(a.plan, unit, it)) return;
+  if (unit >= a.plan.max_items) return;
+  const DecayItem it = decay_item(a.plan, unit);
+  if (it.seq < 0) return;
   if (!OUT && (REV ? it.prev : it.next) < 0) return;  // no boundary behind this item
   const int w = wave_id(), lane = lane_id(), g = lane >> 4, li = lane & 15;
   const int w0 = 16 * NB * w;  // this wave's first state column
@@ -759,6 +812,14 @@ __global__ __launch_bounds__(256) void decay_chain_kernel(DecayChainArgs a) {
     if (m >= a.plan.table[1]) return;
     const int* e = a.plan.table + kDecayHead + a.plan.max_items * kDecayItem + m * kDecayMulti;
     seq = e[0], slot0 = e[1], cnt = e[2], last = e[3];
+  } else if (a.plan.seq_start) {
+    const DecaySeqs s(a.plan);
+    unsigned long long in = __ballot(s.cnt > 0);
+    if (m >= __builtin_popcountll(in)) return;
+    for (int i = 0; i < m; ++i) in &= in - 1;
+    seq = __builtin_ctzll(in);
+    slot0 = __builtin_amdgcn_readlane(s.slot0, seq), cnt = __builtin_amdgcn_readlane(s.cnt, seq);
+    last = __builtin_amdgcn_readlane(s.t1 - s.t0, seq) - cnt * a.plan.L;
   } else {
     seq = m, cnt = a.plan.P - 1, slot0 = m * cnt, last = a.plan.T - cnt * a.plan.L;
   }
@@ -807,6 +868,10 @@ __global__ __launch_bounds__(256) void decay_group_kernel(DecayGroupArgs a, int 
   if (a.plan.table) {
     i = (long long)a.plan.table[2] * a.Hk * D4;
     n4 = (long long)a.plan.table[3] * a.Hk * D4;
+  } else if (a.plan.seq_start) {
+    const DecaySeqs s(a.plan);
+    i = (long long)__builtin_amdgcn_readlane(s.t0, 0) * a.Hk * D4;
+    n4 = (long long)__builtin_amdgcn_readlane(s.t1, a.plan.n_seq - 1) * a.Hk * D4;
   }
   for (i += (long long)blockIdx.x * 256 + threadIdx.x; i < n4; i += (long long)gridDim.x * 256) {
     const long long row = i / D4;
@@ -818,11 +883,10 @@ __global__ __launch_bounds__(256) void decay_group_kernel(DecayGroupArgs a, int 
 }
 
 // -------------------------------------------------------------------- launch
-static hipError_t decay_plan(const DecayPlan& p, const int* seq_start, int n_seq, int n_tok,
-                             hipStream_t st, Profiler* prof) {
+static hipError_t decay_plan(const DecayPlan& p, hipStream_t st, Profiler* prof) {
   if (!p.table) return hipSuccess;
   prof_begin(prof, "decay_plan", st);
-  hipLaunchKernelGGL(decay_plan_kernel, dim3(1), dim3(1024), 0, st, seq_start, n_seq, n_tok, p);
+  hipLaunchKernelGGL(decay_plan_kernel, dim3(1), dim3(1024), 0, st, p);
   prof_end(prof, st);
   return hipGetLastError();
 }
@@ -885,7 +949,7 @@ static hipError_t decay_chain(const DecayChainArgs& a, int roles, hipStream_t st
 template <typename T, int D>
 hipError_t launch_decay_fwd(const DecayArgs& d, hipStream_t st, Profiler* prof) {
   hipError_t e;
-  if ((e = decay_plan(d.plan, d.seq_start, d.n_seq, d.n_tok, st, prof)) != hipSuccess) return e;
+  if ((e = decay_plan(d.plan, st, prof)) != hipSuccess) return e;
   DecayScanArgs a{};
   a.plan = d.plan;
   a.decay = d.decay;
@@ -909,7 +973,7 @@ hipError_t launch_decay_fwd(const DecayArgs& d, hipStream_t st, Profiler* prof) 
 template <typename T, int D>
 hipError_t launch_decay_bwd(const DecayArgs& d, hipStream_t st, Profiler* prof) {
   hipError_t e;
-  if ((e = decay_plan(d.plan, d.seq_start, d.n_seq, d.n_tok, st, prof)) != hipSuccess) return e;
+  if ((e = decay_plan(d.plan, st, prof)) != hipSuccess) return e;
   const DecayTensor q{d.q, d.qs, 1}, k{d.k, d.ks, 1}, v{d.v, d.vs, 0},
       dO{d.dO, (long long)d.Hv * D, 0};
   const bool part = d.group > 1;

@@ -185,16 +185,20 @@ int residual_norm_groups(long long N, int C);
 
 // Linear attention with a decay for each head (see gdn_decay.hpp).
 //
-// A call's segments.  Sequences of one length (table null): T tokens in P
-// segments of L.  Packed ones: a table of ints on the device, written by the
-// call's first kernel,
+// A call's segments.  Sequences of one length (table and seq_start null): T
+// tokens in P segments of L.  Packed ones, up to kDecayLanes: from seq_start, by
+// each wave that wants to know; more: a table of ints on the device, written by
+// the call's first kernel,
 //   [0] boundaries, [1] sequences of several segments, [2], [3] the rows they
 //   have, max_items items of {sequence, first token, tokens, boundary slots
 //   before and after it (-1: none)}, max_multi of {sequence, first boundary
 //   slot, boundaries, tokens of the last segment}.
 constexpr int kDecayHead = 4, kDecayItem = 5, kDecayMulti = 4;
+constexpr int kDecayLanes = 64;  // sequences that a wave plans by itself
 struct DecayPlan {
   int* table;
+  const int* seq_start;
+  int n_seq, n_tok;
   int L, T, P;
   int max_items, max_slots, max_multi;
 };
@@ -244,7 +248,6 @@ struct DecayArgs {
   const void* k;
   const void* v;
   const float* decay;
-  const int* seq_start;
   const float* S_in;
   void* o;
   float* S_out;
@@ -255,7 +258,7 @@ struct DecayArgs {
   void* dv;
   float* dS_in;
   long long qs, ks, vs;
-  int n_seq, n_tok, Hv, group;
+  int n_tok, Hv, group;
   float scale;
   // workspace
   DecayPlan plan;

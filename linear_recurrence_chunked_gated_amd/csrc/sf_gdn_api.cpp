@@ -1230,10 +1230,11 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, bool bwd, DecayCall& 
   // the kernels address a block of 64 rows in 31 bits
   if (a.qs > (1 << 22) || a.ks > (1 << 22) || a.vs > (1 << 22))
     return fail(SF_ERR_UNSUPPORTED, "token rows more than 2^22 elements apart");
-  a.n_seq = p->n_seq; a.n_tok = p->n_tok; a.Hv = p->Hv; a.group = p->Hv / p->Hk;
+  a.n_tok = p->n_tok; a.Hv = p->Hv; a.group = p->Hv / p->Hk;
   a.scale = p->scale;
   DecayPlan& d = a.plan;
   d = DecayPlan{};
+  d.n_seq = p->n_seq; d.n_tok = p->n_tok;
   d.T = !packed && p->n_seq > 0 ? p->n_tok / p->n_seq : p->n_tok;
   const bool f32 = p->dtype == SF_DTYPE_F32;
   long long L = decay_blocks(((long long)p->n_tok + BLK - 1) / BLK * p->Hv, f32, bwd);
@@ -1261,7 +1262,7 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, bool bwd, DecayCall& 
     d.max_items = p->n_seq + (int)c.slots;
     d.max_multi = (int)(c.slots < p->n_seq ? c.slots : p->n_seq);
     d.P = 0;
-    c.table = align_up(sizeof(int) * (kDecayHead + (size_t)d.max_items * kDecayItem +
+    c.table = p->n_seq <= kDecayLanes ? 0 : align_up(sizeof(int) * (kDecayHead + (size_t)d.max_items * kDecayItem +
                                       (size_t)d.max_multi * kDecayMulti));
   } else {
     d.P = d.T > 0 ? (d.T + d.L - 1) / d.L : 1;
@@ -1293,14 +1294,15 @@ sf_status decay_ws_size(const sf_decay_shape* shape, bool bwd, size_t* bytes) {
   return SF_OK;
 }
 
-sf_status carve_decay(DecayCall& c, bool packed, bool bwd, void* workspace, size_t ws_bytes) {
+sf_status carve_decay(DecayCall& c, const int* seq_start, bool bwd, void* workspace, size_t ws_bytes) {
   const size_t need = decay_ws(c, bwd);
   if (need > 0 && (!workspace || ws_bytes < need))
     return fail(SF_ERR_WORKSPACE, "workspace needs " + std::to_string(need) + " bytes");
   if (workspace && ((uintptr_t)workspace % kAlign))
     return fail(SF_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
   char* w = (char*)workspace;
-  if (packed) c.a.plan.table = (int*)w;
+  c.a.plan.seq_start = seq_start;
+  if (c.table > 0) c.a.plan.table = (int*)w;
   w += c.table;
   for (int i = 0; i < 1 + bwd; ++i, w += c.bound) c.a.bound[i] = (float*)w;
   for (int i = 0; bwd && i < 2; ++i, w += c.part) c.a.part[i] = (float*)w;
@@ -1365,7 +1367,7 @@ sf_status sf_gdn_decay_chunk_fwd(const sf_decay_shape* shape, const void* q, con
   if ((s = check_apart(small, out)) != SF_OK) return s;
   if ((s = check_floats(decay, "decay")) != SF_OK) return s;
   if ((s = carve_decay(c, seq_start, false, workspace, ws_bytes)) != SF_OK) return s;
-  a.q = q; a.k = k; a.v = v; a.decay = decay; a.seq_start = seq_start; a.S_in = S_in; a.o = o;
+  a.q = q; a.k = k; a.v = v; a.decay = decay; a.S_in = S_in; a.o = o;
   a.S_out = S_out;
   hipStream_t st = (hipStream_t)stream;
   return run_locked([&](Profiler* prof) -> sf_status {
@@ -1410,7 +1412,7 @@ sf_status sf_gdn_decay_chunk_bwd(const sf_decay_shape* shape, const void* q, con
   if ((s = check_apart(small, out)) != SF_OK) return s;
   if ((s = check_floats(decay, "decay")) != SF_OK) return s;
   if ((s = carve_decay(c, seq_start, true, workspace, ws_bytes)) != SF_OK) return s;
-  a.q = q; a.k = k; a.v = v; a.decay = decay; a.seq_start = seq_start; a.S_in = S_in; a.dO = dO;
+  a.q = q; a.k = k; a.v = v; a.decay = decay; a.S_in = S_in; a.dO = dO;
   a.dS_out = dS_out; a.dq = dq; a.dk = dk; a.dv = dv; a.dS_in = dS_in;
   hipStream_t st = (hipStream_t)stream;
   return run_locked([&](Profiler* prof) -> sf_status {

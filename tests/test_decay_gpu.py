@@ -216,6 +216,33 @@ def test_more_sequences_than_the_plan_takes_at_once():
         assert torch.equal(o1, o[sl]) and torch.equal(S1[0], S[i]), i
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("f32", 64), ("bf16", 128)])
+def test_planned_by_waves_and_by_a_table(dtype, D):
+    """Up to 64 sequences are planned by each wave, more by a table.  Empty
+    sequences behind the others change nothing but that."""
+    lens = [0, 700, 1, 0, 64, 65, 600, 128, 3, 0] + [17] * 40 + [0, 400, 129, 0]
+    n = len(lens)
+    d = chunk_inputs(lens, 1, 2, D, dtype, seed=77, grads=True)
+    c = _cuda(d)
+    (ro, rS), (ob, Sb) = chunk_ref(d)
+    ref, bnd = chunk_bwd_ref(d)
+    outs = []
+    for more in (0, 64 - n, 65 - n, 1100 - n):
+        st = torch.cat([c["seq_start"], c["seq_start"][-1:].expand(more)])
+        ext = lambda x: torch.cat([x, x.new_zeros(more, *x.shape[1:])])
+        m = dict(c, seq_start=st, S_in=ext(c["S_in"]), dS_out=ext(c["dS_out"]))
+        o, S = _fwd(m)
+        g = _bwd(m)
+        outs.append((o, S[:n]) + tuple(g[:3]) + (g[3][:n],))
+        assert not S[n:].any() and not g[3][n:].any()
+    for x, r, b, t in zip(outs[0], (ro, rS) + tuple(ref), (ob, Sb) + tuple(bnd),
+                          (dtype, None, dtype, dtype, dtype, None)):
+        check("packed", x, r, b, t)
+    for other in outs[1:]:
+        for x, y in zip(outs[0], other):
+            assert torch.equal(x, y)
+
+
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 64)])
 def test_long_sequences_and_large_batches(dtype, D):
     """Segments of more than the least four blocks: 20,011 tokens of 16 heads,

@@ -97,14 +97,24 @@ def _bytes(bwd=False, **kw):
     dict(n_seq=1, n_tok=262144, Hk=32, Hv=32),
 ])
 def test_workspace_sizes(kw):
-    """Boundary states of all heads are some hundreds; the table is small."""
+    """Boundary states of all heads are some hundreds, and a backward in bf16
+    has fewer, twice; the table is small, and up to 64 sequences need none."""
     s = _shape(**kw)
     states = (kw.get("n_seq", 2) + 3 * 512) * s.Dk * s.Dv * 4
     table = 4 * (16 + 9 * (s.n_seq + 3 * 512)) + 512
     fwd, bwd = _bytes(**kw), _bytes(True, **kw)
-    assert 0 < fwd <= states + table
-    part = 2 * s.n_tok * s.Hv * s.Dv * 4 + 512 if s.Hv > s.Hk else 0
-    assert fwd <= bwd <= 2 * states + table + part
+    assert (0 if s.n_seq <= 64 else 20 * s.n_seq) <= fwd <= states + table
+    part = 2 * s.n_tok * s.Hv * s.Dv * 4 if s.Hv > s.Hk else 0
+    assert part <= bwd <= 2 * states + table + part + 512
+
+
+def test_rows_too_far_apart():
+    """A block of 64 rows is addressed in 31 bits: strides up to 2^22."""
+    ok, far = 1 << 22, (1 << 22) + 8
+    for name in ("qs", "ks", "vs"):
+        assert _fwd(wsn=0, ws=0, **{name: far}) == UNS
+        assert _bwd(wsn=0, ws=0, **{name: far}) == UNS
+        assert _fwd(wsn=0, ws=0, n_seq=1, n_tok=4096, **{name: ok}) == WS
 
 
 def test_the_caller_may_give_more_workspace_but_not_less():
