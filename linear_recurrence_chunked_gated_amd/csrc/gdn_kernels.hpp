@@ -299,7 +299,7 @@ struct RotaryArgs {
   int D, F, first;
   float eps;
 };
-int rotary_groups(long long N);
+int rotary_groups(long long N, const int (&H)[2], int D);
 
 // Optional per-launch event timing (see sf_gdn_profile_* in the C ABI).
 struct Profiler;

@@ -1512,7 +1512,7 @@ sf_status make_rotary(const sf_rotary_shape* p, const int* pos, RotaryArgs& a) {
 }
 
 size_t rotary_ws(const RotaryArgs& a, int wanted) {
-  return align_up((size_t)rotary_groups(a.N) * a.D * 4 * wanted);
+  return align_up((size_t)rotary_groups(a.N, a.H, a.D) * a.D * 4 * wanted);
 }
 
 // The inputs that both directions read.
