@@ -479,7 +479,6 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
   typedef DecayTile<T, D> Tl;
   constexpr int C = Tl::C, NP = Tl::NP, NY = DecayKind<T>::NY, NT = Tl::NT;
   constexpr int NW = NT / 64, NB = D / 16 / NW, NU = D / 16, KD = D / 32, KT = C / 32, NR = C / 16;
-  constexpr int TILES = NR * (NR + 1) / 2, TPW = (TILES + NW - 1) / NW;  // P tiles, of a wave
   typedef DecayP<C> Pl;
   // LDS (it starts at 0: there is no other): u, w, x, P, then the powers
   constexpr unsigned aU = 0, aW = NP * Tl::BYTES, aX = 2 * aW, aP = 3 * aW;
@@ -554,25 +553,35 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
   lds_barrier();
   // a^(n-1-s) (reversed: a^(s+1)), of whole blocks
   if (threadIdx.x < C) dec[threadIdx.x] = s_pair * pw[REV ? threadIdx.x + 1 : C - 1 - threadIdx.x];
-  // This wave's tiles of P that the mask leaves (m = s, n = r), in turn; a wave
-  // with one fewer does one twice.  pf: the factors, 0 where a diagonal tile is
-  // masked.
-  int pr[TPW], ps[TPW];
+  // This wave's tiles of P that the mask leaves (m = s, n = r): of the operand
+  // rows hi[.] (r; reversed: s) with lo[.] <= hi[.].  Of four rows of tiles, two
+  // waves take the squares at the diagonal and two the rest, a column each, so
+  // that a tile's operands serve two; of two rows a wave takes one tile.  (A
+  // tile that a wave has no use for it does twice.)  pf: the factors, 0 where a
+  // diagonal tile is masked.
+  constexpr int TH = NR / 2, TPW = 2 * TH - 1;
+  int hi[TH], lo[TH];
   float pf[TPW][4];
+  auto tile_h = [](int i) { return TH == 1 ? 0 : i > 0; };
+  auto tile_l = [](int i) { return i / 2; };
   if constexpr (OUT) {
+    if constexpr (TH == 2) {
+      hi[0] = w == 0 ? 0 : 2;
+      lo[0] = w & 2;
+      if (w & 1) lo[0] = w >> 1;
+      hi[1] = hi[0] + 1;
+      lo[1] = lo[0] + (w % 2 == 0);
+    } else {
+      hi[0] = w > 0;
+      lo[0] = w > 1;
+    }
 #pragma unroll
-    for (int i = 0; i < TPW; ++i) {
-      int t = w + NW * i;
-      if (t >= TILES) t = max(t - NW, 0) % TILES;
-      const int hi = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, lo = t - hi * (hi + 1) / 2;
-      pr[i] = REV ? lo : hi;
-      ps[i] = REV ? hi : lo;
+    for (int i = 0; i < TPW; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int d = 16 * (hi - lo) + (REV ? 4 * g + e - li : li - 4 * g - e);
+        const int d = 16 * (hi[tile_h(i)] - lo[tile_l(i)]) + (REV ? 4 * g + e - li : li - 4 * g - e);
         pf[i][e] = d >= 0 ? s_pair * s_out * pw[d] : 0.f;
       }
-    }
   }
 
   typename Tl::Lane ln;
@@ -602,21 +611,25 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
 #pragma unroll
       for (int i = 0; i < TPW; ++i) p[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < KD; ++s)
+      for (int s = 0; s < KD; ++s) {
+        bf16x8 fu[TH][NP], fx[TH][NP];
 #pragma unroll
-        for (int i = 0; i < TPW; ++i) {
-          bf16x8 fu[NP], fx[NP];
-          Tl::rows_std(ln, aU, 16 * ps[i], s, fu);
-          Tl::rows_std(ln, aX, 16 * pr[i], s, fx);
-          p[i] = mma_planes(fu, fx, p[i]);
+        for (int i = 0; i < TH; ++i) {
+          Tl::rows_std(ln, aU, 16 * (REV ? hi : lo)[i], s, fu[i]);
+          Tl::rows_std(ln, aX, 16 * (REV ? lo : hi)[i], s, fx[i]);
         }
+#pragma unroll
+        for (int i = 0; i < TPW; ++i)
+          p[i] = mma_planes(fu[REV ? tile_h(i) : tile_l(i)], fx[REV ? tile_l(i) : tile_h(i)], p[i]);
+      }
 #pragma unroll
       for (int i = 0; i < TPW; ++i) {
         const float q[4] = {p[i][0] * pf[i][0], p[i][1] * pf[i][1], p[i][2] * pf[i][2],
                             p[i][3] * pf[i][3]};
         bf16x4 h[NY];
         to_planes(q, h);
-        Pl::store(lp, aP, pr[i], ps[i], h);
+        const int h_ = hi[tile_h(i)], l_ = lo[tile_l(i)];
+        Pl::store(lp, aP, REV ? l_ : h_, REV ? h_ : l_, h);
       }
       // E x
       zero_acc(O);
