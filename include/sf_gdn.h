@@ -385,17 +385,20 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
  * is a constant of the layer and gets none.
  *
  * In bf16 the masked products q k^T and the state's copy that meets q are
- * rounded to bf16 on the way to o (as the operands of its products), the
- * states are not (2^-17).  fp32 tensors enter the products as pairs of bf16
- * (2^-17 of a term; o, the states and the gradients within about 1e-5 of
- * their norm).  Finite inputs are a precondition: a value that is not finite
- * reaches the outputs of its 64-token block and of the later ones (earlier
- * ones, for gradients) of its sequence, and no other sequence.
+ * rounded to bf16 on the way to o (as the operands of its products); the
+ * states are sums in fp32 of terms rounded to 2^-16, those that are outputs
+ * (S_out, dS_in) of terms rounded as fp32 is.  fp32 tensors enter the products
+ * in three bf16 parts, which hold all of their 24 bits (magnitudes below
+ * 2^127): o, the states and the gradients are as close as sums in fp32.  Finite inputs are a precondition: a value
+ * that is not finite reaches the outputs of its 64-token block and of the later
+ * ones (earlier ones, for gradients) of its sequence, and no other sequence.
  *
- * The workspace (256-byte aligned) holds the table of segments and the states
- * at their boundaries, and for shared key heads in the backward 8 bytes for
- * each element of v.  Calls that may run at the same time need one each.
- * Dk == Dv in {64, 128}; n_tok up to 2^30, n_seq * Hv up to 2^21. */
+ * The workspace (256-byte aligned) holds the states at the segments'
+ * boundaries, for more than 64 packed sequences the table of segments, and for
+ * shared key heads in the backward 8 bytes for each element of v.  Calls that
+ * may run at the same time need one each, two captured ones too.
+ * Dk == Dv in {64, 128}; n_tok up to 2^30, n_seq * Hv up to 2^21, token rows up
+ * to 2^22 elements apart. */
 typedef struct {
   int n_seq, n_tok;
   int Hk, Hv;

@@ -464,10 +464,11 @@ __device__ __forceinline__ void decay_unit(const DecayScanArgs& a, int& role, in
 // [b][c] has m = the u index (16 c ..), n = the w index (16 (NB w + b) ..).
 //
 // Roundings to fewer bits, for bf16 tensors: P and the state's copy that meets
-// x go as bf16 (2^-9), as is usual for operands of outputs that are rounded to
+// x go as bf16 (2^-8), as is usual for operands of outputs that are rounded to
 // bf16 themselves; the state, which goes on from block to block, sums w times
-// its decay in NS = 2 planes (2^-18), and in a third (2^-27) where it ends as an
-// fp32 output, or in a boundary's sum on the way to one.
+// its decay in NS = 2 planes (2^-16), and in a third (2^-24, all of an fp32
+// value) where it ends as an fp32 output, or in a boundary's sum on the way to
+// one.  For fp32 tensors all of these are three planes.
 //
 // OUT: a scan; otherwise the sum for a boundary, which is the same whatever
 // order its blocks come in.  They come in the opposite order of the scan's, so

@@ -2,20 +2,20 @@
 rotation, with error bounds of their kernels beside the values (not a test
 module).
 
-The chunk kernels work in blocks of 64 tokens from each sequence's start:
+The chunk kernels work in blocks of 64 (fp32: 32) tokens:
     y_r = sum_{s <= r} P_rs w_s + a^(r+first) E x_r,   P_rs = a^(r-s) x_r . u_s
-with the state E at the block's start.  H = 2^-8 is half a step of bf16, and
-H^2 what two bf16 planes of an fp32 value leave of it.
+with the state E at the block's start.  H = 2^-8 is half a step of bf16, H^2
+what two bf16 planes of an fp32 value leave of it, and three leave nothing.
 
  bf16 tensors: P and E are rounded to bf16 on the way to y, H of each term; E's
-   own sums have w times its decay in two planes, H^2 of each term.
- fp32 tensors: every operand in two planes and no product of second planes.
-   P: 3 H^2 of the sum of |x||u|; P w: P's and w's planes and their second
-   planes' product, 3 H^2; E x: E's terms 4 H^2 (w, w times its decay, u, and
-   the product), E x itself 3 H^2: at most 7 H^2 of the sum of all terms'
-   absolute values.
- fp32 sums: one U = 2^-24 of the terms' absolute values for each of at most
-   T + 64 additions, and a few for the decays' factors.
+   own sums have w times its decay in two planes, H^2 of each term (the factors
+   of the two compound: 4 H^2 in all), and in three where E ends as an output.
+ fp32 tensors: every operand in three planes, and of the products of planes
+   those down to H^2: the others are 2 H^3 and less.  P, P w, E and E x have
+   one such product each: at most 8 H^3 of the sum of all terms' absolute values
+   (H^3 = 2^-24 = U, what a sum in fp32 rounds to).
+ fp32 sums: one U of the terms' absolute values for each of at most T + 64
+   additions, and a few for the decays' factors.
 """
 import torch
 
@@ -60,14 +60,14 @@ def _blocks(x, u, w, a, E, first, cuts, exact):
         f = (a ** (r + first).double())[:, None]
         y[t:t + n] = P @ W + f * (X @ E.t())
         terms = ((X.abs() @ V.abs().t()) * M.abs()) @ W.abs() + f.abs() * (X.abs() @ A.t())
-        b[t:t + n] = (7 * H * H if exact else 4 * H * H) * terms + (T + 64) * U * terms
+        b[t:t + n] = (8 * U if exact else 4 * H * H) * terms + (T + 64) * U * terms
         if not exact:
             b[t:t + n] += H * (P.abs() @ W.abs() + f.abs() * (X.abs() @ E.abs().t()))
         dec = (a ** (n - r - first).double())[:, None]
         E = a ** n * E + (dec * W).t() @ V
         A = abs(a) ** n * A + (dec.abs() * W.abs()).t() @ V.abs()
         t += n
-    return y, b, E, ((4 if exact else 1) * H * H + (T + 64) * U) * A
+    return y, b, E, (T + 72) * U * A
 
 
 def _cuts(T):
