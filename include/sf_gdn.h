@@ -388,10 +388,11 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
  * rounded to bf16 on the way to o (as the operands of its products); the
  * states are sums in fp32 of terms rounded to 2^-16, those that are outputs
  * (S_out, dS_in) of terms rounded as fp32 is.  fp32 tensors enter the products
- * in three bf16 parts, which hold all of their 24 bits (magnitudes below
- * 2^127): o, the states and the gradients are as close as sums in fp32.  Finite inputs are a precondition: a value
- * that is not finite reaches the outputs of its 64-token block and of the later
- * ones (earlier ones, for gradients) of its sequence, and no other sequence.
+ * in three bf16 parts, which hold all of their 24 bits: o, the states and the
+ * gradients are as close as sums in fp32.  Values and states up to 2^100 in
+ * magnitude are a precondition, finite ones too: a value that is not finite
+ * reaches the outputs of its 64-token block and of the later ones (earlier
+ * ones, for gradients) of its sequence, and no other sequence.
  *
  * The workspace (256-byte aligned) holds the states at the segments'
  * boundaries, for more than 64 packed sequences the table of segments, and for

@@ -38,10 +38,13 @@ constexpr int ROT_WAVES = ROT_THREADS / 64;
 constexpr int ROT_MAX = 256;
 __device__ __forceinline__ void token_turns(const RotaryArgs& a, long long token, float* cs) {
   const int pos = a.pos ? a.pos[token] : a.first + (int)(token % a.T);
+  // a wave's lanes go together: the compiler only has to keep the order
+  __builtin_amdgcn_wave_barrier();
   for (int i = lane_id(); i < a.F; i += 64) {
     const double turns = (double)pos * ((double)a.freq[i] * 0.15915494309189533577);
     sincospif(2.f * (float)(turns - rint(turns)), &cs[ROT_MAX + i], &cs[i]);
   }
+  __builtin_amdgcn_wave_barrier();
 }
 
 // What a lane is in a row of L lanes.

@@ -482,7 +482,7 @@ def test_autograd_against_64_bits():
         got = run("cuda", torch.float32, lambda *a: gdn.decay_chunk(*a, scale=0.5), use)
         ref = run("cpu", torch.float64, lambda *a: _plain(*a, 0.5), use)
         for name, x, r in zip("qkvS", got, ref):
-            # 7 H^2 = 1.1e-4 of the terms bounds it; of the norm it is far less
+            # (72 + 90) U = 1e-5 of the terms bounds a chunk's; two are chained
             assert (x - r).norm() <= 2e-5 * r.norm(), (use, name, float((x - r).norm() / r.norm()))
 
 
