@@ -1174,26 +1174,24 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
 // ------------------------------------- linear attention with a decay per head
 namespace {
 
-// Blocks of a segment.  A workgroup takes one segment (an item) of one value
-// head and, in a backward, one of the three gradients; two share a compute unit.
-// Few blocks in all are spread over 256 workgroups (forward of 1024 tokens of 16
-// heads at D = 128: 1 block a segment 34 us, 4 blocks 44; 4096 tokens: 2 blocks
-// 58 us, 4 blocks 53, 8 blocks 69), more than 8 a segment over 512 (65,536
-// tokens: 438 us, 523 over 256, 462 over 1024, where boundary states, written,
-// chained and read again, cost more).  A backward in bf16 takes a third of that,
-// one round of its three scans (backward of 16,384 tokens of 16 heads 241 us, 262
-// over 512; 24 packed sequences of 16,411 tokens, 32 heads: 505 and 545; but of
-// 65,536 tokens 890 and 857); in fp32, where the scans are bound by
+// Blocks of a segment (64 tokens; 32 in fp32).  A workgroup takes one segment
+// (an item) of one value head and, in a backward, one of the three gradients; two
+// share a compute unit.  Few blocks in all are spread over 256 workgroups (bf16,
+// 16 heads at D = 128: 1024 tokens 36 us with one block a segment, 38 with two, 44
+// with four; 4096 tokens 58 with two, 53 with four, 69 with eight; fp32, 2 heads
+// at D = 64: 256 tokens 18 us with one, 21 with two), more than 512 tokens a
+// segment over 512 (65,536 tokens: 438 us, 523 over 256, 462 over 1024, where
+// boundary states, written, chained and read again, cost more).  A backward in
+// bf16 takes a third of that, one round of its three scans (16,384 tokens of 16
+// heads 241 us, 262 over 512; 24 packed sequences of 16,411 tokens, 32 heads: 505
+// and 545; but 65,536 tokens 890 and 857); in fp32, where the scans are bound by
 // their products, it does not (32,768 tokens 1185 us, 1350 over 170).
-// In bf16 a segment has two blocks at least, and sequences of up to four (fp32:
-// two) are not cut: a block takes less than the two more launches (256 tokens
-// of 2 heads at D = 64: bf16 16 us whole, 20 cut in four; fp32 26 and 21).
 long long decay_blocks(long long blocks, bool f32, bool bwd) {
   auto over = [&](long long groups) { return (blocks + groups - 1) / groups; };
-  const int some = bwd && !f32 ? 170 : 256, all = bwd && !f32 ? 170 : 512;
-  long long L = over(some) < 8 ? over(some) : 8;
+  const int some = bwd && !f32 ? 170 : 256, all = bwd && !f32 ? 170 : 512, few = f32 ? 16 : 8;
+  long long L = over(some) < few ? over(some) : few;
   if (L < over(all)) L = over(all);
-  return L < (f32 ? 1 : 2) ? (f32 ? 1 : 2) : L;
+  return L < 1 ? 1 : L;
 }
 
 struct DecayCall {
@@ -1237,17 +1235,24 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, bool bwd, DecayCall& 
   d.n_seq = p->n_seq; d.n_tok = p->n_tok;
   d.T = !packed && p->n_seq > 0 ? p->n_tok / p->n_seq : p->n_tok;
   const bool f32 = p->dtype == SF_DTYPE_F32;
-  long long L = decay_blocks(((long long)p->n_tok + BLK - 1) / BLK * p->Hv, f32, bwd);
-  const long long own = (d.T + BLK - 1) / BLK;  // blocks of a sequence
-  if (!packed) {
-    // Sequences that are short, or that fill three quarters of the GPU by
-    // themselves, are not cut: there is no pass for boundary states then, and a
-    // workgroup alone on its compute unit is faster (forward of 2048 tokens each,
-    // 16 heads: 12 sequences 150 us, 171 cut, 8 sequences 144 and 115; backward,
-    // three workgroups to a head: 8 sequences 202 us, 277 cut, 4 of 4096 tokens
-    // 276 and 262).
-    if (own <= (f32 ? 2 : 4) || L >= own || (long long)p->n_seq * p->Hv >= (bwd ? 96 : 192)) {
+  const int C = f32 ? 32 : 64;  // tokens of a block
+  long long L = decay_blocks(((long long)p->n_tok + C - 1) / C * p->Hv, f32, bwd);
+  const long long own = (d.T + C - 1) / C;  // blocks of a sequence (packed: at most)
+  // Sequences of a few blocks, or that fill three quarters of the GPU by
+  // themselves, are not cut: there is no pass for boundary states then, and a
+  // workgroup alone on its compute unit is faster (four blocks: bf16 at D = 64
+  // 16.4 us, 18.5 cut in four, fp32 17.7 and 18.3, but at D = 128 29.7 and 24.5;
+  // forward of 2048 tokens each, 16 heads: 12 sequences 150 us, 171 cut, 8
+  // sequences 144 and 115; backward, three workgroups to a head: 8 sequences
+  // 202 us, 277 cut, 4 of 4096 tokens 276 and 262).
+  const bool short_ones = own <= (f32 && D == 128 ? 2 : 4);
+  if (packed) {
+    if (short_ones) L = own > 0 ? own : 1;
+  } else {
+    if (short_ones || L >= own || (long long)p->n_seq * p->Hv >= (bwd ? 96 : 192)) {
       L = own > 0 ? own : 1;
+    } else if (own > 32 && L < 2) {
+      L = 2;  // a longer chain costs more (fp32, 64 blocks of 2 heads: 23 us, 24 with one)
     } else if (!f32 && L >= 8) {
       // the last segment, whose state takes a third plane, gets less than the
       // others (65,536 tokens: the scan 250 us, 287 with segments alike)
@@ -1255,15 +1260,17 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, bool bwd, DecayCall& 
       L = (2 * own + 2 * P - 2) / (2 * P - 1);
     }
   }
-  d.L = (int)(L * BLK);
+  d.L = (int)(L * C);
   if (packed) {
     c.slots = p->n_tok > 0 ? (p->n_tok - 1) / d.L : 0;
     d.max_slots = (int)c.slots;
     d.max_items = p->n_seq + (int)c.slots;
     d.max_multi = (int)(c.slots < p->n_seq ? c.slots : p->n_seq);
     d.P = 0;
-    c.table = p->n_seq <= kDecayLanes ? 0 : align_up(sizeof(int) * (kDecayHead + (size_t)d.max_items * kDecayItem +
-                                      (size_t)d.max_multi * kDecayMulti));
+    c.table = p->n_seq <= kDecayLanes
+                  ? 0
+                  : align_up(sizeof(int) * (kDecayHead + (size_t)d.max_items * kDecayItem +
+                                            (size_t)d.max_multi * kDecayMulti));
   } else {
     d.P = d.T > 0 ? (d.T + d.L - 1) / d.L : 1;
     c.slots = (long long)p->n_seq * (d.P - 1);
