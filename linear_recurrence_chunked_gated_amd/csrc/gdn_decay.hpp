@@ -476,12 +476,15 @@ __device__ __forceinline__ void decay_unit(const DecayScanArgs& a, int& role, in
 // Four waves and two workgroups a compute unit, at up to 256 registers: the
 // state, O and the next block's rows fill them (eight waves with half the columns
 // each were slower, their operand reads twice as many).  Measured in bf16 at
-// D = 128: 65,536 tokens of 16 heads take 135 us for the sums (4.0 TB/s) and 249
-// for the scan (4.3 TB/s); a block takes 7.3 to 7.8 us of a workgroup's time
-// whatever its heads share (16 key heads for 32: 2.9 TB/s), with the matrix units
-// busy for 26% of it, the vector units for 38% and LDS for 40%: the chain of
-// steps between barriers bounds it, not one of them.  fp32 (six products for
-// one) 880 us for both, bound by the products.
+// D = 128: 65,536 tokens of 16 heads take 137 us for the sums (3.9 TB/s) and 240
+// to 250 for the scan (4.5 TB/s); a block takes 7.3 to 7.8 us of a workgroup's
+// time whatever its heads share (16 key heads for 32: 2.9 TB/s), with the matrix
+// units busy for 29% of it, the vector units for 38% and LDS for 45%: the chain
+// of steps between barriers bounds it, not one of them.  (A third of LDS's cycles
+// are bank conflicts, most of them of the transpose reads, whose rows r and r + 1
+// meet; a swizzle that moves rows by pairs of units ends those, and with two
+// more spilled registers was no faster: scan 243-247 us, sums 139-141.)  fp32
+// (six products for one) 880 us for both, bound by the products.
 //
 // OUT: a scan; otherwise the sum for a boundary, which is the same whatever
 // order its blocks come in.  They come in the opposite order of the scan's, so

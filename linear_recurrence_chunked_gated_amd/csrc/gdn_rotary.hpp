@@ -21,8 +21,9 @@
 // in 64.
 //
 // Measured (bf16, 16 + 16 heads of 128): forward of 32,768 tokens 99 us (5.4
-// TB/s), backward of 62,720 tokens 272 us (5.7 TB/s), as fast as a copy of as
-// many bytes; one token 4.9 us, its backward 7.5, what a launch (two) takes.
+// TB/s), backward of 62,720 tokens 266 us (5.8 TB/s), as fast as a copy of as
+// many bytes; one token 5 to 6 us, its backward 7.5, what a launch (two) takes
+// (3.2 us replayed from a graph).
 #pragma once
 #include "gdn_norm.hpp"
 
