@@ -20,7 +20,8 @@
 // of all heads fill the GPU:
 //   decay_sum     every inner boundary's sum over the segment before it (after
 //                 it, reversed), from zero
-//   decay_chain   those to the states at the boundaries, one after another
+//   decay_chain   those to the states at the boundaries, one after another; where
+//                 there are few, every item does that for its own boundary
 //   decay_scan    every item from its entry state: the outputs, and the last
 //                 (first) item's exit state
 // with the scans of all roles in one launch, and so the sums (dv's and dk's
@@ -31,9 +32,10 @@
 namespace sfgdn {
 
 // One item: a segment of a sequence.  prev, next: the boundary slots before
-// and after it (-1 at the sequence's ends).
+// and after it (-1 at the sequence's ends).  Without a table: how many
+// boundaries there are before and after it, and the last segment's tokens.
 struct DecayItem {
-  int seq, t0, n, prev, next;
+  int seq, t0, n, prev, next, before, after, last;
 };
 
 // Packed sequences: offsets are taken as their running maximum, clamped to the
@@ -77,7 +79,7 @@ struct DecaySeqs {
 __device__ __forceinline__ DecayItem decay_item(const DecayPlan& p, int i) {
   if (p.table) {
     const int* e = p.table + kDecayHead + i * kDecayItem;
-    return DecayItem{i >= p.table[0] && i < p.max_slots ? -1 : e[0], e[1], e[2], e[3], e[4]};
+    return DecayItem{i >= p.table[0] && i < p.max_slots ? -1 : e[0], e[1], e[2], e[3], e[4], 0, 0, 0};
   }
   int seq, t0, len, first, cnt, j;
   if (p.seq_start) {
@@ -109,8 +111,9 @@ __device__ __forceinline__ DecayItem decay_item(const DecayPlan& p, int i) {
     cnt = p.P - 1;
     first = seq * cnt;
   }
-  return DecayItem{seq, t0 + j * p.L, j < cnt ? p.L : len - cnt * p.L, j > 0 ? first + j - 1 : -1,
-                   j < cnt ? first + j : -1};
+  const int last = len - cnt * p.L;
+  return DecayItem{seq, t0 + j * p.L, j < cnt ? p.L : last, j > 0 ? first + j - 1 : -1,
+                   j < cnt ? first + j : -1, j, cnt - j, last};
 }
 
 // a^e for e >= 0, by squaring in 64 bits: exact to a rounding for every a,
@@ -537,27 +540,42 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
     const float* E = nullptr;
     bool tr = R.tr_state;
     if (OUT) {
-      if (slot >= 0) {
+      if (slot >= 0 && !a.plan.direct) {
         E = R.bound + ((size_t)slot * a.Hv + hv) * D * D;
         tr = R.tr_bound;
       } else if (R.state) {
         E = R.state + ((size_t)it.seq * a.Hv + hv) * D * D;
       }
     }
+    auto entry = [&](const float* E, bool tr, int b, int c) {
+      const int m = 16 * c + 4 * g, n = w0 + 16 * b + li;
+      f32x4 x = {0.f, 0.f, 0.f, 0.f};
+      if (E && tr) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = E[(size_t)(m + e) * D + n];
+      } else if (E) {
+        x = *reinterpret_cast<const f32x4*>(E + (size_t)n * D + m);
+      }
+      return x;
+    };
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int c = 0; c < NU; ++c) {
-        const int m = 16 * c + 4 * g, n = w0 + 16 * b + li;
-        f32x4 x = {0.f, 0.f, 0.f, 0.f};
-        if (E && tr) {
+      for (int c = 0; c < NU; ++c) St[b][c] = entry(E, tr, b, c);
+    if (OUT && slot >= 0 && a.plan.direct) {  // the chain up to this item's boundary
+      const float aL = decay_pow(alpha, a.plan.L);
+      float f = REV ? decay_pow(alpha, it.last) : aL;
+      const int n = REV ? it.after : it.before;
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const float* B = R.bound + ((size_t)(REV ? slot + n - 1 - i : slot - n + 1 + i) * a.Hv + hv) * D * D;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = E[(size_t)(m + e) * D + n];
-        } else if (E) {
-          x = *reinterpret_cast<const f32x4*>(E + (size_t)n * D + m);
-        }
-        St[b][c] = x;
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int c = 0; c < NU; ++c) St[b][c] = St[b][c] * f + entry(B, R.tr_bound, b, c);
+        f = aL;
       }
+    }
   }
 
   // powers; P tiles that the mask empties but a product of 32 tokens reads
@@ -993,7 +1011,7 @@ hipError_t launch_decay_fwd(const DecayArgs& d, hipStream_t st, Profiler* prof) 
     c.decay = d.decay;
     c.Hv = d.Hv;
     c.role[0] = DecayChainRole{d.bound[0], d.S_in, 0, 0};
-    if ((e = decay_chain<D>(c, 1, st, prof)) != hipSuccess) return e;
+    if (!d.plan.direct && (e = decay_chain<D>(c, 1, st, prof)) != hipSuccess) return e;
   }
   return decay_scans<T, D>(a, false, d.S_out, st, prof);
 }
@@ -1028,7 +1046,7 @@ hipError_t launch_decay_bwd(const DecayArgs& d, hipStream_t st, Profiler* prof) 
     c.Hv = d.Hv;
     c.role[0] = DecayChainRole{d.bound[0], d.S_in, 1, 0};
     c.role[1] = DecayChainRole{d.bound[1], d.dS_out, 0, 1};
-    if ((e = decay_chain<D>(c, 2, st, prof)) != hipSuccess) return e;
+    if (!d.plan.direct && (e = decay_chain<D>(c, 2, st, prof)) != hipSuccess) return e;
   }
   a.roles = 3;
   if ((e = decay_scans<T, D>(a, true, d.dS_in, st, prof)) != hipSuccess) return e;

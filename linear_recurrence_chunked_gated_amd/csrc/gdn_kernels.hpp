@@ -201,6 +201,7 @@ struct DecayPlan {
   int n_seq, n_tok;
   int L, T, P;
   int max_items, max_slots, max_multi;
+  int direct;  // each item joins its sequence's boundary sums by itself
 };
 struct DecayTensor {
   const void* p;

@@ -1278,6 +1278,16 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, bool bwd, DecayCall& 
     d.max_multi = d.P > 1 ? p->n_seq : 0;
     c.table = 0;
   }
+  // The boundaries that an item may have to join by itself (packed: all of them
+  // may be one sequence's) save the chain's launch, but come one after another:
+  // up to three, and in a packed batch, where they are usually spread, up to a
+  // segment's blocks (bf16 at D = 128: 4 sequences of 1600 tokens, 3 each, 52 us,
+  // 56 with the chain, backward 102 and 112; 24 packed prompts, 15 in all, 161 and
+  // 174, 195 and 190 if one has them all; 6 packed ones of 12,000 tokens, backward,
+  // 10 in all, 179 and 186, 176 and 172; but one of 4096 tokens, 7: 66 and 49).
+  const long long joins = packed ? c.slots : d.P - 1, blocks = d.L / C;
+  d.direct = c.table == 0 &&
+             (joins <= 3 || (packed && p->n_seq > 1 && joins <= 16 && joins <= blocks));
   c.bound = align_up((size_t)c.slots * p->Hv * D * D * 4);
   c.part = a.group > 1 ? align_up((size_t)p->n_tok * p->Hv * D * 4) : 0;
   return SF_OK;

@@ -200,3 +200,30 @@ def _refused():
 def test_refused(what):
     with pytest.raises((ValueError, RuntimeError, TypeError)):
         _refused()[what]()
+
+
+@pytest.mark.parametrize("lens,Hk,Hv,D,dtype", [
+    ([130], 1, 1, 128, "bf16"), ([70, 1, 90], 2, 4, 64, "f32"), ([300, 0, 257], 1, 2, 128, "f32"),
+    ([7000, 300, 9, 1003], 4, 16, 64, "bf16"),  # backward: 10 boundaries, segments of 13 blocks
+    ([1, 5, 16990, 4], 8, 32, 64, "bf16"),      # forward: one sequence has nearly all of them
+    ([4000, 3900, 4100, 3], 16, 32, 128, "bf16"),
+])
+def test_boundaries_joined_by_the_items_and_by_the_chain(lens, Hk, Hv, D, dtype):
+    """Few boundaries are joined by every item for itself, more (and those of
+    more than 64 sequences, most of them empty here) by a kernel: one result."""
+    d = chunk_inputs(lens, Hk, Hv, D, dtype, seed=261 + sum(lens), grads=True)
+    c, n = _cuda(d), len(lens)
+    more = 65 - n
+    ext = lambda x: torch.cat([x, x.new_zeros(more, *x.shape[1:])])
+    m = dict(c, seq_start=torch.cat([c["seq_start"], c["seq_start"][-1:].expand(more)]),
+             S_in=ext(c["S_in"]), dS_out=ext(c["dS_out"]))
+
+    def run(x):
+        o, S = gdn.decay_chunk_fwd(x["q"], x["k"], x["v"], x["decay"], x["S_in"], x["seq_start"])
+        g = gdn.decay_chunk_bwd(x["q"], x["k"], x["v"], x["decay"], x["S_in"], x["dO"],
+                                x["dS_out"], x["seq_start"])
+        torch.cuda.synchronize()
+        return (o, S[:n]) + tuple(g[:3]) + (g[3][:n],)
+
+    for x, y in zip(run(c), run(m)):
+        assert torch.isfinite(x).all() and torch.equal(x, y)
