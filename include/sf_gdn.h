@@ -384,10 +384,10 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
  * (summed over the value heads of a key head, in order), v and S_in.  The decay
  * is a constant of the layer and gets none.
  *
- * In bf16 the masked products q k^T and the state's copy that meets q are
- * rounded to bf16 on the way to o (as the operands of its products); the
- * states are sums in fp32 of terms rounded to 2^-16, those that are outputs
- * (S_out, dS_in) of terms rounded as fp32 is.  fp32 tensors enter the products
+ * In bf16 the masked products q k^T and the state's copy that meets q enter
+ * the products for o in two bf16 parts (2^-16), so that o and the gradients are
+ * off by their own rounding; the states are sums in fp32 of terms rounded to
+ * 2^-16, those that are outputs (S_out, dS_in) of terms rounded as fp32 is.  fp32 tensors enter the products
  * in three bf16 parts, which hold all of their 24 bits: o, the states and the
  * gradients are as close as sums in fp32.  Values and states up to 2^100 in
  * magnitude are a precondition, finite ones too: a value that is not finite
