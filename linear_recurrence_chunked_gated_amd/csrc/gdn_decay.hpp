@@ -507,7 +507,7 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
   constexpr unsigned aU = 0, aW = NP * Tl::BYTES, aX = 2 * aW, aP = 3 * aW;
   constexpr unsigned aF = OUT ? aP + NY * Pl::BYTES : aX;
   extern __shared__ __align__(16) unsigned char smem[];
-  float* pw = reinterpret_cast<float*>(smem + aF);  // a^0 .. a^C
+  float* pw = reinterpret_cast<float*>(smem + aF);  // a^0 .. a^C, and what a^C's rounding left
   float* dec = pw + C + 4;                          // [C]
 
   if (unit >= a.plan.max_items) return;
@@ -583,7 +583,11 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
 
   // powers; P tiles that the mask empties but a product of 32 tokens reads
   const float s_pair = R.s_pair, s_out = R.s_out;
-  if (threadIdx.x <= C) pw[threadIdx.x] = decay_pow(alpha, threadIdx.x);
+  if (threadIdx.x <= C) {
+    const double p = decay_pow64(alpha, threadIdx.x);
+    pw[threadIdx.x] = (float)p;
+    if (threadIdx.x == C) pw[C + 1] = (float)(p - (double)(float)p);
+  }
   if constexpr (OUT) {
     for (int i = threadIdx.x; i < NY * Pl::BYTES / 16; i += NT)
       *lds_at<u32x4>(aP + 16 * i) = u32x4{0, 0, 0, 0};
@@ -628,7 +632,10 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
   const bool exact = R.exit && (REV ? it.prev : it.next) < 0;  // the state ends as an output
   // A scan's state is St times `frame`, which takes the blocks' decays until it
   // leaves 2^-20 .. 2^20 (a sum's block has the decay between it and the
-  // boundary instead).
+  // boundary instead).  Both take a block's decay in 64 bits (48, in two floats,
+  // for a scan: a double in registers makes the instances at D = 128 spill): rounded
+  // to fp32 it is off to the same side in every block, over hundreds of them by
+  // more than the sums' roundings.
   double frame = 1.0, far = 1.0;
   for (int i = 0; i < nblk; ++i) {
     const int blk = DOWN ? nblk - 1 - i : i;
@@ -697,7 +704,7 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
     // w of this wave's columns: for P w, and scaled for the state
     float fd;
     if constexpr (OUT) {
-      frame *= (double)pw[nv];
+      frame *= (double)pw[nv] + (nv == C ? (double)pw[C + 1] : 0.0);
       if (!(frame > 0x1p-20 && frame < 0x1p20)) {
         const float f = (float)frame;
 #pragma unroll

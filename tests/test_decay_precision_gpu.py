@@ -6,7 +6,7 @@ import torch
 
 import linear_recurrence_chunked_gated_amd as gdn
 from decay_testutil import H, chunk_bwd_ref, chunk_inputs, chunk_ref
-from layer_testutil import U, check
+from layer_testutil import DT, U, check
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +33,28 @@ def test_bf16_outputs_are_off_by_their_own_rounding(T, Hk, Hv, D):
     for name, x, r, b in zip(("o", "dq", "dk", "dv"), (o,) + got[:3], (ro,) + ref, (ob,) + bnd):
         terms = b / ((T + 72) * U)
         check(name, x, r, (4 * H * H + (T + 64) * U) * terms, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_a_states_decay_over_many_blocks(dtype):
+    """192 heads of 8192 tokens (not cut: 128 or 256 blocks each) that add
+    nothing to the state: S_out = a^T S_in, and dS_in = a^T dS_out.  The blocks'
+    decays are taken together in 48 bits at least, so the result has a rounding
+    of the decay and one of the product whenever it is taken into the state,
+    which is for every 2^-20 of it and at the end: (2 folds + 2) U, however
+    many blocks there are.  (Blocks' decays rounded to fp32 are off by up to
+    154 U and 92 U here.)"""
+    T, H, B = 8192, 24, 8
+    dt = DT[dtype]
+    decay = (1 - 2.0 ** -torch.linspace(7, 14, H)).cuda()
+    S = torch.randn(B, H, 64, 64, generator=torch.Generator().manual_seed(311)).cuda()
+    q = torch.ones(B, T, 1, 64, dtype=dt, device="cuda")
+    none, v = torch.zeros_like(q), torch.zeros(B, T, H, 64, dtype=dt, device="cuda")
+    aT = decay.double() ** T
+    folds = torch.floor(-torch.log2(aT) / 20) + 1
+    want = aT[:, None, None] * S.double()
+    lim = ((2 * folds + 2) * U + 2.0 ** -40)[:, None, None] * want.abs()
+    _, S_out = gdn.decay_chunk_fwd(q, none, v, decay, S)
+    assert ((S_out.double() - want).abs() <= lim).all()
+    dS = gdn.decay_chunk_bwd(none, q, v, decay, None, v, S)[3]
+    assert ((dS.double() - want).abs() <= lim).all()
