@@ -129,6 +129,23 @@ __device__ __forceinline__ double decay_pow64(float a, int e) {
 }
 __device__ __forceinline__ float decay_pow(float a, int e) { return (float)decay_pow64(a, e); }
 
+// A segment's decay in 48 bits, and a boundary's state behind it: x a^n + sum.
+// (In fp32 it is off to the same side at every boundary of a long chain.)
+struct DecayFactor {
+  float hi, lo;
+  __device__ __forceinline__ DecayFactor(float a, int n) {
+    const double p = decay_pow64(a, n);
+    hi = (float)p;
+    lo = (float)(p - (double)hi);
+  }
+  __device__ __forceinline__ f32x4 join(f32x4 x, f32x4 sum) const {
+    f32x4 y;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = __builtin_fmaf(x[e], hi, __builtin_fmaf(x[e], lo, sum[e]));
+    return y;
+  }
+};
+
 // ------------------------------------------------------------------ the plan
 // Items and boundary slots of more packed sequences, by one workgroup.
 template <typename F>
@@ -566,8 +583,8 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
 #pragma unroll
       for (int c = 0; c < NU; ++c) St[b][c] = entry(E, tr, b, c);
     if (OUT && slot >= 0 && a.plan.direct) {  // the chain up to this item's boundary
-      const float aL = decay_pow(alpha, a.plan.L);
-      float f = REV ? decay_pow(alpha, it.last) : aL;
+      const DecayFactor aL(alpha, a.plan.L);
+      DecayFactor f = REV ? DecayFactor(alpha, it.last) : aL;
       const int n = REV ? it.after : it.before;
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
@@ -575,7 +592,7 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int c = 0; c < NU; ++c) St[b][c] = St[b][c] * f + entry(B, R.tr_bound, b, c);
+          for (int c = 0; c < NU; ++c) St[b][c] = f.join(St[b][c], entry(B, R.tr_bound, b, c));
         f = aL;
       }
     }
@@ -881,8 +898,8 @@ __global__ __launch_bounds__(256) void decay_chain_kernel(DecayChainArgs a) {
   }
   const int at = part * 1024 + threadIdx.x * 4;
   const float alpha = a.decay[hv];
-  const float aL = decay_pow(alpha, a.plan.L);
-  float f = R.rev ? decay_pow(alpha, last) : aL;
+  const DecayFactor aL(alpha, a.plan.L);
+  DecayFactor f = R.rev ? DecayFactor(alpha, last) : aL;
   f32x4 X = {0.f, 0.f, 0.f, 0.f};
   if (R.state) {
     const float* E = R.state + ((size_t)seq * a.Hv + hv) * D * D;
@@ -906,7 +923,7 @@ __global__ __launch_bounds__(256) void decay_chain_kernel(DecayChainArgs a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int j = j0 + u;
-      X = X * f + n[u];
+      X = f.join(X, n[u]);
       f = aL;
       if (j < cnt) *reinterpret_cast<f32x4*>(p + (size_t)(R.rev ? cnt - 1 - j : j) * pitch) = X;
     }
