@@ -1247,7 +1247,7 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, bool bwd, DecayCall& 
   // 202 us, 277 cut, 4 of 4096 tokens 276 and 262).
   const bool short_ones = own <= (f32 && D == 128 ? 2 : 4);
   if (packed) {
-    if (short_ones) L = own > 0 ? own : 1;
+    if (short_ones || L > own) L = own > 0 ? own : 1;  // (none is longer than the rows)
   } else {
     if (short_ones || L >= own || (long long)p->n_seq * p->Hv >= (bwd ? 96 : 192)) {
       L = own > 0 ? own : 1;

@@ -217,3 +217,20 @@ def test_calls_refuse_cpu_tensors():
               lambda: gdn.qk_norm_rotary(x, x), lambda: gdn.qk_norm_rotary_bwd(x, x, None, None, w, w, x, x)):
         with pytest.raises(ValueError, match="GPU"):
             f()
+
+
+@pytest.mark.parametrize("n_seq,n_tok,Hk,Hv,D,dtype", [
+    (1, 1 << 30, 2048, 2048, 64, 1), (1, 1 << 28, 8192, 8192, 128, 1), (1, 1 << 30, 512, 512, 128, 1),
+    (1, 1 << 30, 1, 1 << 16, 64, 0), (3, (1 << 30) - 1, 3, 48, 64, 1), (64, (1 << 30) - 37, 171, 513, 64, 0),
+    (1 << 5, 1 << 30, 1 << 10, 1 << 16, 64, 1), (1 << 21, 1 << 30, 1, 1, 128, 0),
+])
+def test_plans_of_the_largest_batches(n_seq, n_tok, Hk, Hv, D, dtype):
+    """Segments are no longer than the batch, whatever the limits allow: a
+    segment's tokens stay in 32 bits and the boundaries some hundreds."""
+    kw = dict(n_seq=n_seq, n_tok=n_tok, Hk=Hk, Hv=Hv, Dk=D, Dv=D, dtype=dtype)
+    states = (n_seq + 3 * 512) * D * D * 4
+    table = 4 * (16 + 9 * (n_seq + 3 * 512)) + 512
+    part = 2 * n_tok * Hv * D * 4 if Hv > Hk else 0
+    fwd, bwd = _bytes(**kw), _bytes(True, **kw)
+    assert fwd <= states + table
+    assert part <= bwd <= 2 * states + table + part + 512
