@@ -377,7 +377,8 @@ sf_status sf_gdn_residual_norm_bwd(const sf_residual_norm_shape* shape, const vo
  *   q, k [n_tok, Hk, Dk], v [n_tok, Hv, Dv] dtype, token rows stride elements
  *   apart as in the step calls; o, dO, dq, dk, dv contiguous; value head h
  *   reads q and k of head h / (Hv / Hk); decay [Hv] fp32, any value (meant for
- *   0 .. 1; 0 keeps each token's own term only); S_in, S_out, dS_out, dS_in
+ *   0 .. 1; 0 keeps each token's own term only; past 1 its powers up to a
+ *   sequence's length count as values, see below); S_in, S_out, dS_out, dS_in
  *   [n_seq, Hv, Dv, Dk] fp32.  NULL S_in / dS_out mean zeros; NULL S_out /
  *   dS_in mean not wanted.
  * The backward writes the gradients of <dO, o> + <dS_out, S_out> in q, k

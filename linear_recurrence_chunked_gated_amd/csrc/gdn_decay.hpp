@@ -601,7 +601,9 @@ __device__ __forceinline__ void decay_scan_item(const DecayScanArgs& a, const De
   // powers; P tiles that the mask empties but a product of 32 tokens reads
   const float s_pair = R.s_pair, s_out = R.s_out;
   if (threadIdx.x <= C) {
-    const double p = decay_pow64(alpha, threadIdx.x);
+    // (past the item's tokens none is used, but would meet the zeros behind them:
+    // one that overflows would make those NaN)
+    const double p = threadIdx.x <= it.n ? decay_pow64(alpha, threadIdx.x) : 0.0;
     pw[threadIdx.x] = (float)p;
     if (threadIdx.x == C) pw[C + 1] = (float)(p - (double)(float)p);
   }
