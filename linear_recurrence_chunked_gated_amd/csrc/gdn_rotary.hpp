@@ -91,7 +91,10 @@ template <int L, bool NB> struct RotLane {
       p[j] = NB ? v[j ^ 1]
                 : __int_as_float(__builtin_amdgcn_ds_bpermute(other, __float_as_int(v[j])));
 #pragma unroll
-    for (int j = 0; j < NORM_V; ++j) v[j] = v[j] * co[j] + p[j] * si[j];
+    for (int j = 0; j < NORM_V; ++j) {
+      const float y = v[j] * co[j] + p[j] * si[j];
+      v[j] = in ? y : v[j];  // (as it was: 0 times a value that is not finite is NaN)
+    }
   }
 };
 
