@@ -1515,7 +1515,7 @@ sf_status make_rotary(const sf_rotary_shape* p, const int* pos, RotaryArgs& a) {
     return fail(SF_ERR_UNSUPPORTED, "F must be a multiple of 8 (of 4 with neighbours)");
   if (!(p->eps >= 0.f)) return fail(SF_ERR_INVALID_ARG, "eps must be >= 0");
   if (!pos && p->N > 0 && p->T <= 0) return fail(SF_ERR_INVALID_ARG, "without pos T must be positive");
-  if (!pos && p->T > 0 && p->first + (p->T - 1) > INT32_MAX)
+  if (!pos && p->T > 0 && p->T - 1 > (long long)INT32_MAX - p->first)
     return fail(SF_ERR_UNSUPPORTED, "positions past 2^31 - 1");
   // heads of a token are counted in 32 bits, and their elements too
   const long long heads = (long long)p->Hq + p->Hk;

@@ -234,3 +234,13 @@ def test_plans_of_the_largest_batches(n_seq, n_tok, Hk, Hv, D, dtype):
     fwd, bwd = _bytes(**kw), _bytes(True, **kw)
     assert fwd <= states + table
     assert part <= bwd <= 2 * states + table + part + 512
+
+
+@pytest.mark.parametrize("first,T", [((1 << 31) - 2, (1 << 63) - 1), (1, (1 << 63) - 1), (0, (1 << 31) + 1),
+                                     ((1 << 31) - 8, 9), (-5, (1 << 31) + 6), (-(1 << 31), (1 << 63) - 1)])
+def test_positions_past_32_bits_are_refused(first, T):
+    """Without pos the last position is first + T - 1, whatever T's size."""
+    assert _rfwd(pos=None, first=first, T=T) == UNS
+    assert _rbwd(pos=None, first=first, T=T) == UNS
+    ok = (1 << 31) - first  # the last position is 2^31 - 1: refused for its missing freq
+    assert _rfwd(pos=None, first=first, T=ok, freq=None) == INV
