@@ -2,10 +2,10 @@
 
 Argument marshalling only: torch provides device memory and the stream, and
 every step of the computation runs in the library's HIP kernels.  There is no
-fallback: if the library is missing or fails, calls raise.  The decoding calls
-and the norms, whose kernels are shorter than their marshalling in Python,
-check and call through the native module _calls (csrc/sf_gdn_calls.cpp) on the
-same entry points.
+fallback: if the library is missing or fails, calls raise.  The decoding calls,
+the norms, linear attention with a decay and the rotation, whose kernels can be
+shorter than their marshalling in Python, check and call through the native
+module _calls (csrc/sf_gdn_calls.cpp) on the same entry points.
 
 Every call takes ``stream``, the current one when None.  On another, its
 kernels are in no order with the current stream's work but what the caller sets

@@ -60,7 +60,7 @@ template <typename F> __device__ __forceinline__ int wave_scan(int x, int ident,
 
 // Up to 64 sequences, one a lane: every wave plans for itself, which takes less
 // than a kernel before the others would (9 sequences, 4099 tokens in all, 6 heads
-// at D = 64 in fp32: 37 us with one, 33 so; backward 57 and 53).
+// at D = 64 in fp32: 33.6 us with one, 28.6 so; backward 51 and 47).
 struct DecaySeqs {
   int t0, t1, cnt, slot0;  // its rows, its whole segments before the last, their first slot
   __device__ __forceinline__ DecaySeqs(const DecayPlan& p) {
@@ -498,16 +498,18 @@ __device__ __forceinline__ void decay_unit(const DecayScanArgs& a, int& role, in
 //
 // Four waves and two workgroups a compute unit, at up to 256 registers: the
 // state, O and the next block's rows fill them (eight waves with half the columns
-// each were slower, their operand reads twice as many).  Measured in bf16 at
-// D = 128: 65,536 tokens of 16 heads take 137 us for the sums (3.9 TB/s) and 240
-// to 250 for the scan (4.5 TB/s); a block takes 7.3 to 7.8 us of a workgroup's
-// time whatever its heads share (16 key heads for 32: 2.9 TB/s), with the matrix
-// units busy for 29% of it, the vector units for 38% and LDS for 45%: the chain
-// of steps between barriers bounds it, not one of them.  (A third of LDS's cycles
-// are bank conflicts, most of them of the transpose reads, whose rows r and r + 1
-// meet; a swizzle that moves rows by pairs of units ends those, and with two
-// more spilled registers was no faster: scan 243-247 us, sums 139-141.)  fp32
-// (six products for one) 880 us for both, bound by the products.
+// each were slower, their operand reads twice as many; of the instances at
+// D = 128 those whose items all end in an output spill 6 to 9 registers).
+// Measured in bf16 at D = 128: 65,536 tokens of 16 heads take 137 us for the sums
+// (4.2 TB/s) and 283 for the scan (3.9 TB/s); a block takes 8.9 us of a
+// workgroup's time, with the matrix units busy for 37% of it (32% where 32 heads
+// share 16 key heads: 3.1 TB/s), the vector units for 48% and LDS for 44%: the
+// chain of steps between barriers bounds it, not one of them.  (A third of LDS's
+// cycles are bank conflicts, most of them of the transpose reads, whose rows r and
+// r + 1 meet; a swizzle that moves rows by pairs of units ends those, and with two
+// more spilled registers was no faster: scan 243-247 us for 243-249, with P and
+// the state's copy in one plane.)  fp32 (six products for one) 890 us for both,
+// bound by the products.
 //
 // OUT: a scan; otherwise the sum for a boundary, which is the same whatever
 // order its blocks come in.  They come in the opposite order of the scan's, so
@@ -984,7 +986,7 @@ static hipError_t decay_scan(DecayScanArgs a, const char* name, hipStream_t st, 
 // Planes of the state (bf16): three in sums for a state that is an output, and
 // in scans where every item ends in one (no sequence is cut); where few do, they
 // take the third by themselves and the others save it (backward of 32,768
-// tokens, 16 heads, D = 128: 503 us, 534 with three).  A scan of dq ends in none.
+// tokens, 16 heads, D = 128: 512 us, 547 with three).  A scan of dq ends in none.
 template <typename T, int D>
 static hipError_t decay_sums(const DecayScanArgs& a, bool bwd, bool exit, hipStream_t st, Profiler* prof) {
   if constexpr (sizeof(T) == 4)

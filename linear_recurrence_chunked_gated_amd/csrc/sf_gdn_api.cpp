@@ -1177,15 +1177,16 @@ namespace {
 // Blocks of a segment (64 tokens; 32 in fp32).  A workgroup takes one segment
 // (an item) of one value head and, in a backward, one of the three gradients; two
 // share a compute unit.  Few blocks in all are spread over 256 workgroups (bf16,
-// 16 heads at D = 128: 1024 tokens 36 us with one block a segment, 38 with two, 44
-// with four; 4096 tokens 58 with two, 53 with four, 69 with eight; fp32, 2 heads
-// at D = 64: 256 tokens 18 us with one, 21 with two), more than 512 tokens a
-// segment over 512 (65,536 tokens: 438 us, 523 over 256, 462 over 1024, where
-// boundary states, written, chained and read again, cost more).  A backward in
-// bf16 takes a third of that, one round of its three scans (16,384 tokens of 16
-// heads 241 us, 262 over 512; 24 packed sequences of 16,411 tokens, 32 heads: 505
-// and 545; but 65,536 tokens 890 and 857); in fp32, where the scans are bound by
-// their products, it does not (32,768 tokens 1185 us, 1350 over 170).
+// 16 heads at D = 128: 1024 tokens 32 us with one block a segment, 35 with two, 47
+// with four; 4096 tokens 57 with two, 51 with four, 73 with eight; fp32, 2 heads
+// at D = 64: 256 tokens 13.7 us with one, 16.4 with two and no chain), more than
+// 512 tokens a segment over 512 (65,536 tokens: 400 us, 440 over 256, 423 over
+// 1024, where boundary states, written, chained and read again, cost more).  A
+// backward in bf16 takes a third of that, one round of its three scans (16,384
+// tokens of 16 heads 265 us, 293 over 512; 24 packed sequences of 16,411 tokens,
+// 32 heads: 550 and 600; but 65,536 tokens 1000 and 996); in fp32, where the scans
+// are bound by their products, it does not (32,768 tokens 1187 us, 1260 over 170).
+// (Times of calls replayed from a graph, here and below.)
 long long decay_blocks(long long blocks, bool f32, bool bwd) {
   auto over = [&](long long groups) { return (blocks + groups - 1) / groups; };
   const int some = bwd && !f32 ? 170 : 256, all = bwd && !f32 ? 170 : 512, few = f32 ? 16 : 8;
@@ -1240,11 +1241,12 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, bool bwd, DecayCall& 
   const long long own = (d.T + C - 1) / C;  // blocks of a sequence (packed: at most)
   // Sequences of a few blocks, or that fill three quarters of the GPU by
   // themselves, are not cut: there is no pass for boundary states then, and a
-  // workgroup alone on its compute unit is faster (four blocks: bf16 at D = 64
-  // 16.4 us, 18.5 cut in four, fp32 17.7 and 18.3, but at D = 128 29.7 and 24.5;
-  // forward of 2048 tokens each, 16 heads: 12 sequences 150 us, 171 cut, 8
-  // sequences 144 and 115; backward, three workgroups to a head: 8 sequences
-  // 202 us, 277 cut, 4 of 4096 tokens 276 and 262).
+  // workgroup alone on its compute unit is faster (four blocks of 2 and of 16
+  // heads: bf16 at D = 64 12.6 and 13.0 us, cut in four 13.5 and 13.1, at D = 128
+  // 24.1 and 25.7; fp32 at D = 64 13.3 and 13.4, cut 13.1 and 12.7, at D = 128 25.4
+  // and 25.2; forward of 2048 tokens each, 16 heads: 12 sequences 166 us, 187 cut,
+  // 8 sequences 162 and 126; backward, three workgroups to a head: 8 sequences
+  // 233 us, 274 cut, 4 of 4096 tokens 316 and 281).
   const bool short_ones = own <= (f32 && D == 128 ? 2 : 4);
   if (packed) {
     if (short_ones || L > own) L = own > 0 ? own : 1;  // (none is longer than the rows)
@@ -1252,10 +1254,10 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, bool bwd, DecayCall& 
     if (short_ones || L >= own || (long long)p->n_seq * p->Hv >= (bwd ? 96 : 192)) {
       L = own > 0 ? own : 1;
     } else if (own > 32 && L < 2) {
-      L = 2;  // a longer chain costs more (fp32, 64 blocks of 2 heads: 23 us, 24 with one)
+      L = 2;  // a longer chain costs more (fp32, 64 blocks of 2 heads: 19.2 us, 20.0 with one)
     } else if (!f32 && L >= 8) {
       // the last segment, whose state takes a third plane, gets less than the
-      // others (65,536 tokens: the scan 250 us, 287 with segments alike)
+      // others (65,536 tokens: 400 us, 425 with segments alike)
       const long long P = (own + L - 1) / L;
       L = (2 * own + 2 * P - 2) / (2 * P - 1);
     }
@@ -1281,10 +1283,15 @@ sf_status make_decay(const sf_decay_shape* p, bool packed, bool bwd, DecayCall& 
   // The boundaries that an item may have to join by itself (packed: all of them
   // may be one sequence's) save the chain's launch, but come one after another:
   // up to three, and in a packed batch, where they are usually spread, up to a
-  // segment's blocks (bf16 at D = 128: 4 sequences of 1600 tokens, 3 each, 52 us,
-  // 56 with the chain, backward 102 and 112; 24 packed prompts, 15 in all, 161 and
-  // 174, 195 and 190 if one has them all; 6 packed ones of 12,000 tokens, backward,
-  // 10 in all, 179 and 186, 176 and 172; but one of 4096 tokens, 7: 66 and 49).
+  // segment's blocks, but no more than 16.  bf16 at D = 128, with the chain in
+  // brackets: 4 sequences of 1600 tokens, 3 each, 58 us (61), backward 118 (130);
+  // one of 4096 tokens, 7, would take 70 (51).  Packed, spread over the sequences
+  // and all of them one's: 5 (9000 tokens of 32 heads, backward) 272 (285) and 300
+  // (301); 10 (12,000 tokens of 16 heads, backward) 192 (205) and 212 (209),
+  // (40,000 tokens, backward) 748 (754) and 811 (797); 15 (24 prompts of 16,411
+  // tokens, 32 heads) 195 (203) and 228 (221).  Past the limit it would go on like
+  // that, with more to lose: 23 (12,000 tokens) 107 (116) and 141 (108), 31 (40,000
+  // tokens) 260 (272) and 286 (245).
   const long long joins = packed ? c.slots : d.P - 1, blocks = d.L / C;
   d.direct = c.table == 0 &&
              (joins <= 3 || (packed && p->n_seq > 1 && joins <= 16 && joins <= blocks));
